@@ -400,6 +400,89 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
                            void* y, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The same layer for the few tokens of a decoding step (papernotes.org,
+ * 损失函数 / 训练策略; gist.science §4 for the inference cost):
+ *   y = x W_Q^T + alpha z F^T, z = FWHT(x)/d_in, 0 <= T <= QWHA_DECODE_MAX_T
+ * tokens (QWHA_ERR_SHAPE beyond: qwha_layer_fwd's tiles are the better fit
+ * there). Weights, adapter and widths as qwha_layer_fwd (d_in >= 64, group >=
+ * 32); x [T][d_in] and y [T][d_out] share `act`, QWHA_BF16 or QWHA_F32. The
+ * codes are read once for all tokens. Sums are fp32; fp32 x enters with its
+ * 24 bits, a bf16 y is rounded once. p = 0 is the base layer alone (row_ptr, E
+ * and c are then not read and may be NULL). Workspace:
+ * qwha_layer_decode_workspace_bytes(T, d_in, d_out, p) bytes (0 when out of
+ * range), 256-byte aligned; calls that may overlap need one each.
+ * --------------------------------------------------------------------------- */
+enum { QWHA_DECODE_MAX_T = 64 };
+size_t qwha_layer_decode_workspace_bytes(int64_t T, int32_t d_in, int32_t d_out, int64_t p);
+qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t d_in,
+                              int32_t d_out, const uint32_t* codes, const float* scales,
+                              const float* zeros, int32_t bits, int32_t group, int64_t p,
+                              const int32_t* row_ptr, const int32_t* E, const float* c,
+                              float alpha, void* y, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A quantized key/value cache in pages: the weights' code format for what the
+ * decoded tokens add, with the Walsh-Hadamard transform (papernotes.org,
+ * 关键设计 1) over each head's columns, which spreads a channel that stands out
+ * over the row, so that one step and zero per row hold it.
+ *
+ * Arrays, caller-owned; part 0 holds keys, part 1 values:
+ *   codes  uint32 [2][n_pages][heads][page][head_dim * bits / 32], code j of a
+ *          row in word j / cpw at bit (j % cpw) * bits, cpw = 32 / bits;
+ *   scales, zeros  fp32 [2][n_pages][heads][page].
+ * bits is 4 or 8, head_dim 64, 128 or 256, page a power of two in [8, 1024],
+ * n_pages * page <= 2^31 - 1. Token position `off` of page g is slot
+ * g * page + off. `rotate` (0 or 1) must be the same in every call on a cache.
+ *
+ * qwha_cache_write: rows k[t][h][:] and v[t][h][:] (fp32 or bf16, [T][heads]
+ *   [head_dim]) into slot slots[t]. With n = head_dim, x a row and
+ *   v = fp32(x H / n) (rotate) or x:
+ *     lo = min(v, 0), hi = max(v, 0), s = fp32(fp32(hi - lo) / (2^b - 1)),
+ *     z = floor(-lo / s + 1/2), q = clip(floor(v / s + 1/2) + z, 0, 2^b - 1),
+ *   the transform in fp64 and both floors as exact arithmetic on the fp32 v
+ *   and s gives them. A step below 2^-126 stores s = z = q = 0. A slot outside
+ *   [0, n_pages * page) is skipped (padding). The slots of one call that are
+ *   not skipped must be distinct (not checked; two tokens on one slot leave a
+ *   mixture of both there and touch nothing else).
+ * qwha_cache_read: k[t][h][:] and v[t][h][:] (fp32 or bf16) of slot slots[t]:
+ *   s (q - z), times H with rotate; zeros for a slot outside the cache. Slots
+ *   may repeat.
+ * qwha_cache_attn: attention of one query token per sequence,
+ *     out[b][i] = sum_t softmax_t(scale q[b][i] . k_t) v_t  over t < lens[b],
+ *   k_t and v_t the rows read back (without being written out) of key/value
+ *   head i / (q_heads / heads) in page table[b][t / page] at t % page; q and
+ *   out [B][q_heads][head_dim] in `act`, table int32 [B][width], lens int32
+ *   [B]. Sums and the softmax are fp32, fp32 queries enter with their 24 bits.
+ *   lens[b] <= 0 gives a row of zeros, lens[b] above width * page counts as
+ *   width * page, and the tokens of a table entry outside [0, n_pages) are
+ *   left out. Nothing at or behind lens[b] is used, whatever it holds.
+ *   Requires heads to divide q_heads, 0 <= B <= 65535. Workspace:
+ *   qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
+ *   bytes (0 when out of range), 256-byte aligned; calls that may overlap
+ *   need one each.
+ * Values read (k, v, q, and the cache's rows in use) must be finite, as for
+ * every call here; others spoil their own rows only. Out-of-range slots and
+ * pages are checked on the device and never read or written through.
+ * --------------------------------------------------------------------------- */
+qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64_t T,
+                             const int32_t* slots, int32_t heads, int32_t head_dim, int32_t bits,
+                             int32_t rotate, int64_t n_pages, int32_t page, uint32_t* codes,
+                             float* scales, float* zeros, hipStream_t stream);
+qwha_status qwha_cache_read(const uint32_t* codes, const float* scales, const float* zeros,
+                            int32_t heads, int32_t head_dim, int32_t bits, int32_t rotate,
+                            int64_t n_pages, int32_t page, const int32_t* slots, int64_t T,
+                            qwha_dtype out_dtype, void* k, void* v, hipStream_t stream);
+size_t qwha_cache_attn_workspace_bytes(int32_t B, int32_t q_heads, int32_t heads,
+                                       int32_t head_dim, int32_t width, int32_t page);
+qwha_status qwha_cache_attn(const void* q, qwha_dtype act, int32_t B, int32_t q_heads,
+                            const uint32_t* codes, const float* scales, const float* zeros,
+                            int32_t heads, int32_t head_dim, int32_t bits, int32_t rotate,
+                            int64_t n_pages, int32_t page, const int32_t* table, int32_t width,
+                            const int32_t* lens, float scale, void* out, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Profiling aid: the next launch of kernel `kernel` made by this thread
  * (inside any entry point above) is bracketed by hipEventRecord(start) and
  * hipEventRecord(stop) on that launch's stream; the request is then
@@ -424,7 +507,11 @@ typedef enum qwha_kernel {
   QWHA_KERNEL_CALIB_SYSTEM = 13,  /* rhs gather and G inside qwha_init_select_calibrated */
   QWHA_KERNEL_REFINE = 14,      /* the per-row solves of qwha_refine_values */
   QWHA_KERNEL_MERGE = 15,       /* qwha_merge */
-  QWHA_KERNEL_QGEMM = 16        /* the base GEMM inside qwha_layer_fwd */
+  QWHA_KERNEL_QGEMM = 16,       /* the base GEMM inside qwha_layer_fwd */
+  QWHA_KERNEL_LAYER_DECODE = 17, /* the product inside qwha_layer_decode */
+  QWHA_KERNEL_CACHE_WRITE = 18, /* qwha_cache_write */
+  QWHA_KERNEL_CACHE_READ = 19,  /* qwha_cache_read */
+  QWHA_KERNEL_CACHE_ATTN = 20   /* qwha_cache_attn */
 } qwha_kernel;
 qwha_status qwha_profile_next(int32_t kernel, hipEvent_t start, hipEvent_t stop);
 

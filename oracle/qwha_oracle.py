@@ -71,7 +71,7 @@ __all__ = [
     "init_select_calibrated", "layer_output_error", "unpack_codes", "dequantize",
     "merge_weights", "layer_forward", "scatter_dense",
     "materialize", "forward", "backward", "backward_dc_rows", "sign_update",
-    "rel_err",
+    "rel_err", "cache_quantize", "cache_dequantize", "attend",
 ]
 
 
@@ -574,6 +574,53 @@ def layer_forward(x: np.ndarray, W_Q: np.ndarray, E: np.ndarray, c: np.ndarray,
     """y = x W_Q^T + alpha z F^T (fp64): the quantized layer with its
     adapter, by the plain definition x (W_Q + alpha F H^-1)^T."""
     return np.asarray(x, dtype=np.float64) @ merge_weights(W_Q, E, c, alpha).T
+
+
+# --------------------------------------------------------------------------
+# The quantized key/value cache: rows of head_dim values, one step and zero a
+# row, and one query token's attention over them
+# --------------------------------------------------------------------------
+
+def cache_quantize(x: np.ndarray, bits: int, rotate: bool):
+    """(codes, s, z) of rows x [..., n]: v = fp32(x H / n) (rotate) or x; over
+    v's range with zero included s = fp32(fp32(hi - lo) / (2^b - 1)),
+    z = floor(-lo/s + 1/2), q = clip(floor(v/s + 1/2) + z, 0, 2^b - 1). The
+    quotients are of fp32 numbers: fp64 separates them from the next half
+    (|v - (k + 1/2) s| is 0 or at least 2^-25 s), so both floors are exact. A step
+    below fp32's smallest normal number stores zeros."""
+    x = np.asarray(x, dtype=np.float64)
+    n = x.shape[-1]
+    qmax = float(2 ** bits - 1)
+    v = (x @ sylvester(n) / n if rotate else x).astype(np.float32).astype(np.float64)
+    lo = np.minimum(v.min(axis=-1, keepdims=True), 0.0)
+    hi = np.maximum(v.max(axis=-1, keepdims=True), 0.0)
+    s = ((hi - lo).astype(np.float32).astype(np.float64) / qmax).astype(np.float32)
+    s = np.where(s < np.finfo(np.float32).tiny, np.float32(0), s).astype(np.float64)
+    by = np.where(s > 0, s, 1.0)
+    z = np.where(s > 0, np.floor(-lo / by + 0.5), 0.0)
+    q = np.where(s > 0, np.clip(np.floor(v / by + 0.5) + z, 0, qmax), 0.0)
+    return q.astype(np.uint8), s[..., 0], z[..., 0]
+
+
+def cache_dequantize(q: np.ndarray, s: np.ndarray, z: np.ndarray, rotate: bool) -> np.ndarray:
+    """Rows read back: s (q - z), times H with rotate (fp64)."""
+    v = (q.astype(np.float64) - np.asarray(z, np.float64)[..., None]) * \
+        np.asarray(s, np.float64)[..., None]
+    return v @ sylvester(q.shape[-1]) if rotate else v
+
+
+def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float) -> np.ndarray:
+    """One sequence: q [q_heads][n] over k and v [tokens][heads][n], query head
+    i reading head i / (q_heads / heads); zeros over no tokens (fp64)."""
+    out = np.zeros(q.shape, dtype=np.float64)
+    if k.shape[0] == 0:
+        return out
+    per = q.shape[0] // k.shape[1]
+    for i in range(q.shape[0]):
+        a = scale * (k[:, i // per].astype(np.float64) @ q[i].astype(np.float64))
+        e = np.exp(a - a.max())
+        out[i] = (e / e.sum()) @ v[:, i // per].astype(np.float64)
+    return out
 
 
 # --------------------------------------------------------------------------

@@ -52,6 +52,23 @@ SIGNATURES = {
                                  c_void_p, c_void_p, c_int32, c_int32, c_int64, c_void_p,
                                  c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_size_t,
                                  c_void_p]),
+    "qwha_layer_decode_workspace_bytes": (c_size_t, [c_int64, c_int32, c_int32, c_int64]),
+    "qwha_layer_decode": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_int32, c_void_p,
+                                    c_void_p, c_void_p, c_int32, c_int32, c_int64, c_void_p,
+                                    c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_size_t,
+                                    c_void_p]),
+    "qwha_cache_write": (c_int32, [c_void_p, c_void_p, c_int32, c_int64, c_void_p, c_int32,
+                                   c_int32, c_int32, c_int32, c_int64, c_int32, c_void_p,
+                                   c_void_p, c_void_p, c_void_p]),
+    "qwha_cache_read": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                  c_int32, c_int64, c_int32, c_void_p, c_int64, c_int32,
+                                  c_void_p, c_void_p, c_void_p]),
+    "qwha_cache_attn_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_int32, c_int32,
+                                                   c_int32]),
+    "qwha_cache_attn": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                                  c_void_p, c_int32, c_int32, c_int32, c_int32, c_int64, c_int32,
+                                  c_void_p, c_int32, c_void_p, c_float, c_void_p, c_void_p,
+                                  c_size_t, c_void_p]),
     "qwha_materialize": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int64,
                                    c_float, c_int32, c_void_p, c_int32, c_void_p]),
     "qwha_fwd_workspace_bytes": (c_size_t, [c_int64, c_int32, c_int32, c_int64]),

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/qwha.h"
+#include "cache.h"
 #include "launch.h"
 
 using namespace qwha;
@@ -42,7 +43,7 @@ size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 struct Hook {
   hipEvent_t start, stop;
 };
-constexpr int kNumKernelIds = 17;
+constexpr int kNumKernelIds = 21;
 thread_local Hook g_hook[kNumKernelIds] = {};
 
 // Runs `launch` (a callable returning hipError_t) for kernel id `k`, with the
@@ -589,6 +590,192 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
                                                qw, y32, static_cast<uint16_t*>(y), stream);
                          }),
                    "base gemm");
+}
+
+size_t qwha_layer_decode_workspace_bytes(int64_t T, int32_t d_in, int32_t d_out, int64_t p) {
+  if (T < 0 || T > QWHA_DECODE_MAX_T || d_in < 1 || d_out < 1 || p < 0) return 0;
+  return align256(static_cast<size_t>(T) * d_in * 4);
+}
+
+qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t d_in,
+                              int32_t d_out, const uint32_t* codes, const float* scales,
+                              const float* zeros, int32_t bits, int32_t group, int64_t p,
+                              const int32_t* row_ptr, const int32_t* E, const float* c,
+                              float alpha, void* y, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  g_err[0] = 0;
+  int log_n;
+  int nblk;
+  QWHA_TRY(check_width(d_out, d_in, &log_n, &nblk));
+  if (d_in < 64) return fail(QWHA_ERR_SHAPE, "d_in=%d below 64", d_in);
+  QWHA_TRY(check_p(p, d_out, d_in));
+  QWHA_TRY(check_dt(act, "act"));
+  QWHA_TRY(check_quant(bits, group, d_in, 32));
+  if (T < 0 || T > QWHA_DECODE_MAX_T)
+    return fail(QWHA_ERR_SHAPE, "T=%lld outside [0, %d] (qwha_layer_fwd takes more tokens)",
+                static_cast<long long>(T), static_cast<int>(QWHA_DECODE_MAX_T));
+  if (!isfinite(alpha)) return fail(QWHA_ERR_INVALID_ARG, "alpha must be finite");
+  QWHA_NEED(codes, 16);
+  QWHA_NEED(scales, 4);
+  QWHA_NEED(zeros, 4);
+  if (p > 0) {
+    QWHA_NEED(row_ptr, 4);
+    QWHA_NEED(E, 4);
+    QWHA_NEED(c, 4);
+  }
+  if (T == 0) return QWHA_OK;
+  QWHA_NEED(x, 16);
+  QWHA_NEED(y, 16);
+  const size_t total = qwha_layer_decode_workspace_bytes(T, d_in, d_out, p);
+  if (workspace == nullptr || workspace_bytes < total)
+    return fail(QWHA_ERR_WORKSPACE, "layer decode workspace needs %zu bytes", total);
+  QWHA_NEED(workspace, 256);
+
+  float* z = nullptr;
+  if (p > 0) {
+    z = static_cast<float*>(workspace);
+    QWHA_TRY(hip_check(launch_fwht(x, static_cast<Dt>(act), z, Dt::F32, T * nblk, log_n,
+                                   1.0f / static_cast<float>(1 << log_n), 0, stream),
+                       "layer fwht"));
+  }
+  const QuantW qw = make_quant(codes, scales, zeros, bits, group, d_in);
+  return hip_check(timed(QWHA_KERNEL_LAYER_DECODE, stream,
+                         [&] {
+                           return launch_decode(x, static_cast<Dt>(act), static_cast<int>(T), d_in,
+                                                d_out, qw, z, row_ptr, E, c, alpha, y, stream);
+                         }),
+                   "layer decode");
+}
+
+// ------------------------------------------------------------------ key/value cache
+static qwha_status check_cache(int32_t heads, int32_t head_dim, int32_t bits, int32_t rotate,
+                               int64_t n_pages, int32_t page, int* lg_page) {
+  if (heads < 1 || heads > 4096) return fail(QWHA_ERR_SHAPE, "heads=%d outside [1, 4096]", heads);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(QWHA_ERR_SHAPE, "head_dim=%d is not one of 64, 128, 256", head_dim);
+  if (bits != 4 && bits != 8)
+    return fail(QWHA_ERR_INVALID_ARG, "bits=%d: the cache holds 4- or 8-bit codes", bits);
+  if (rotate != 0 && rotate != 1)
+    return fail(QWHA_ERR_INVALID_ARG, "rotate=%d is neither 0 nor 1", rotate);
+  if (page < 8 || page > 1024 || (page & (page - 1)) != 0)
+    return fail(QWHA_ERR_SHAPE, "page=%d is not a power of two in [8, 1024]", page);
+  *lg_page = log2_pow2(page);
+  if (n_pages < 1 || n_pages > INT32_MAX / page)
+    return fail(QWHA_ERR_SHAPE, "n_pages=%lld: n_pages * page outside [1, 2^31 - 1]",
+                static_cast<long long>(n_pages));
+  return QWHA_OK;
+}
+
+// rows of a dense [T][2][heads] view, counted in int32 by the launches
+static qwha_status check_cache_tokens(int64_t T, int32_t heads) {
+  if (T < 0 || T > INT32_MAX / (2 * static_cast<int64_t>(heads)))
+    return fail(QWHA_ERR_SHAPE, "T=%lld: T * 2 * heads outside [0, 2^31 - 1]",
+                static_cast<long long>(T));
+  return QWHA_OK;
+}
+
+qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64_t T,
+                             const int32_t* slots, int32_t heads, int32_t head_dim, int32_t bits,
+                             int32_t rotate, int64_t n_pages, int32_t page, uint32_t* codes,
+                             float* scales, float* zeros, hipStream_t stream) {
+  g_err[0] = 0;
+  int lg_page;
+  QWHA_TRY(check_cache(heads, head_dim, bits, rotate, n_pages, page, &lg_page));
+  QWHA_TRY(check_dt(act, "act"));
+  QWHA_TRY(check_cache_tokens(T, heads));
+  QWHA_NEED(codes, 16);
+  QWHA_NEED(scales, 4);
+  QWHA_NEED(zeros, 4);
+  if (T == 0) return QWHA_OK;
+  QWHA_NEED(k, 16);
+  QWHA_NEED(v, 16);
+  QWHA_NEED(slots, 4);
+  const Cache c{codes, scales, zeros, n_pages, lg_page, heads, head_dim, bits};
+  return hip_check(timed(QWHA_KERNEL_CACHE_WRITE, stream,
+                         [&] {
+                           return launch_cache_write(k, v, static_cast<Dt>(act), T, slots, rotate,
+                                                     c, stream);
+                         }),
+                   "cache write");
+}
+
+qwha_status qwha_cache_read(const uint32_t* codes, const float* scales, const float* zeros,
+                            int32_t heads, int32_t head_dim, int32_t bits, int32_t rotate,
+                            int64_t n_pages, int32_t page, const int32_t* slots, int64_t T,
+                            qwha_dtype out_dtype, void* k, void* v, hipStream_t stream) {
+  g_err[0] = 0;
+  int lg_page;
+  QWHA_TRY(check_cache(heads, head_dim, bits, rotate, n_pages, page, &lg_page));
+  QWHA_TRY(check_dt(out_dtype, "out_dtype"));
+  QWHA_TRY(check_cache_tokens(T, heads));
+  QWHA_NEED(codes, 16);
+  QWHA_NEED(scales, 4);
+  QWHA_NEED(zeros, 4);
+  if (T == 0) return QWHA_OK;
+  QWHA_NEED(slots, 4);
+  QWHA_NEED(k, 16);
+  QWHA_NEED(v, 16);
+  const Cache c{const_cast<uint32_t*>(codes), const_cast<float*>(scales),
+                const_cast<float*>(zeros), n_pages, lg_page, heads, head_dim, bits};
+  return hip_check(timed(QWHA_KERNEL_CACHE_READ, stream,
+                         [&] {
+                           return launch_cache_read(c, slots, T, rotate,
+                                                    static_cast<Dt>(out_dtype), k, v, stream);
+                         }),
+                   "cache read");
+}
+
+size_t qwha_cache_attn_workspace_bytes(int32_t B, int32_t q_heads, int32_t heads,
+                                       int32_t head_dim, int32_t width, int32_t page) {
+  if (B < 0 || B > 65535 || heads < 1 || heads > 4096 || q_heads < 1 || q_heads > 65535 ||
+      q_heads % heads != 0 || width < 1 || page < 8 || page > 1024 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  return align256(cache_attn_scratch_bytes(B, q_heads, heads, head_dim,
+                                           static_cast<int64_t>(width) * page));
+}
+
+qwha_status qwha_cache_attn(const void* q, qwha_dtype act, int32_t B, int32_t q_heads,
+                            const uint32_t* codes, const float* scales, const float* zeros,
+                            int32_t heads, int32_t head_dim, int32_t bits, int32_t rotate,
+                            int64_t n_pages, int32_t page, const int32_t* table, int32_t width,
+                            const int32_t* lens, float scale, void* out, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream) {
+  g_err[0] = 0;
+  int lg_page;
+  QWHA_TRY(check_cache(heads, head_dim, bits, rotate, n_pages, page, &lg_page));
+  QWHA_TRY(check_dt(act, "act"));
+  if (B < 0 || B > 65535) return fail(QWHA_ERR_SHAPE, "B=%d outside [0, 65535]", B);
+  if (q_heads < 1 || q_heads > 65535 || q_heads % heads != 0)
+    return fail(QWHA_ERR_SHAPE, "q_heads=%d is not a multiple of heads=%d in [1, 65535]", q_heads,
+                heads);
+  if (width < 1 || static_cast<int64_t>(width) * page > INT32_MAX)
+    return fail(QWHA_ERR_SHAPE, "width=%d: width * page outside [1, 2^31 - 1]", width);
+  if (!isfinite(scale)) return fail(QWHA_ERR_INVALID_ARG, "scale must be finite");
+  QWHA_NEED(codes, 16);
+  QWHA_NEED(scales, 4);
+  QWHA_NEED(zeros, 4);
+  if (B == 0) return QWHA_OK;
+  QWHA_NEED(q, 16);
+  QWHA_NEED(table, 4);
+  QWHA_NEED(lens, 4);
+  QWHA_NEED(out, 16);
+  const size_t total =
+      qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page);
+  if (total > 0) {
+    if (workspace == nullptr || workspace_bytes < total)
+      return fail(QWHA_ERR_WORKSPACE, "cache attention workspace needs %zu bytes", total);
+    QWHA_NEED(workspace, 256);
+  }
+  const Cache c{const_cast<uint32_t*>(codes), const_cast<float*>(scales),
+                const_cast<float*>(zeros), n_pages, lg_page, heads, head_dim, bits};
+  return hip_check(timed(QWHA_KERNEL_CACHE_ATTN, stream,
+                         [&] {
+                           return launch_cache_attn(q, static_cast<Dt>(act), B, q_heads, c, table,
+                                                    width, lens, scale, rotate, out, workspace,
+                                                    stream);
+                         }),
+                   "cache attention");
 }
 
 // ------------------------------------------------------------------ materialize
@@ -1142,7 +1329,7 @@ qwha_status qwha_fwht(const void* in, qwha_dtype in_dtype, void* out, qwha_dtype
 
 qwha_status qwha_profile_next(int32_t kernel, hipEvent_t start, hipEvent_t stop) {
   g_err[0] = 0;
-  if (kernel < QWHA_KERNEL_NONE || kernel > QWHA_KERNEL_QGEMM ||
+  if (kernel < QWHA_KERNEL_NONE || kernel > QWHA_KERNEL_CACHE_ATTN ||
       kernel >= kNumKernelIds)
     return fail(QWHA_ERR_INVALID_ARG, "unknown kernel id %d", kernel);
   if (kernel == QWHA_KERNEL_NONE) {

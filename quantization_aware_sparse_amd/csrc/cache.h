@@ -1,0 +1,43 @@
+// The paged key/value cache as the kernels see it.
+#pragma once
+
+#include <type_traits>
+
+#include "common.h"
+#include "launch.h"
+
+namespace qwha {
+
+// codes [2][n_pages][heads][page][words], scales and zeros
+// [2][n_pages][heads][page]: keys (part 0), then values. A head's tokens of a
+// page lie together, so that attention reads a head's rows in whole lines.
+struct Cache {
+  uint32_t* codes;
+  float* scales;
+  float* zeros;
+  int64_t n_pages;
+  int lg_page;
+  int heads;
+  int dim, bits;
+
+  // rows of one part; the offsets of a long cache pass 32 bits
+  __host__ __device__ int64_t part_rows() const { return (n_pages * heads) << lg_page; }
+  __host__ __device__ int64_t row_in(int part, int32_t page, int off, int head) const {
+    return (((part * n_pages + page) * heads + head) << lg_page) + off;
+  }
+  __host__ __device__ int64_t row(int part, int32_t slot, int head) const {
+    return row_in(part, slot >> lg_page, slot & ((1 << lg_page) - 1), head);
+  }
+};
+
+// q_heads / heads query heads read each head; max_tokens = width * page
+size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t max_tokens);
+hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,
+                              const int32_t* slots, int rotate, const Cache& c, hipStream_t s);
+hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, int rotate, Dt dt,
+                             void* k, void* v, hipStream_t s);
+hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cache& c,
+                             const int32_t* table, int width, const int32_t* lens, float scale,
+                             int rotate, void* out, void* scratch, hipStream_t s);
+
+}  // namespace qwha

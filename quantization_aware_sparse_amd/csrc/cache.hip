@@ -1,0 +1,410 @@
+// The quantized key/value cache: rows written, read back, and attended to.
+//
+// A row is the head_dim values of one token's key or value of one head. With
+// the transform on, what is stored is v = fp32(x H / n), n = head_dim, H the
+// Sylvester matrix (QWHA notes, papernotes.org, 关键设计 1): H spreads a
+// channel that stands out over the whole row, so that one scale and zero per
+// row suffice. v is quantized to b bits over its range with zero included:
+//   lo = min(v, 0), hi = max(v, 0), s = fp32(fp32(hi - lo) / (2^b - 1)),
+//   z = floor(-lo/s + 1/2), q = clip(floor(v/s + 1/2) + z, 0, 2^b - 1),
+// and read back as x' = s (q - z) H.
+#include "cache.h"
+
+namespace qwha {
+
+namespace {
+
+// Lanes of a row hold 16 consecutive columns each; N / 16 lanes a row.
+// Partner lanes of the butterflies, through DPP within rows of 16 lanes:
+// lane ^ 1 and ^ 2 are quad permutes, ^ 4 is the mirror of half a row
+// (lane ^ 7) after the reversal of each quad (lane ^ 3), ^ 8 a rotation by 8.
+template <int X>
+__device__ __forceinline__ int lane_xor_i32(int v) {
+  if constexpr (X == 1) return dpp_i32<0xB1>(v);
+  else if constexpr (X == 2) return dpp_i32<0x4E>(v);
+  else if constexpr (X == 4) return dpp_i32<0x141>(dpp_i32<0x1B>(v));
+  else return dpp_i32<0x128>(v);
+}
+template <int X>
+__device__ __forceinline__ float lane_xor(float v) {
+  return __int_as_float(lane_xor_i32<X>(__float_as_int(v)));
+}
+template <int X>
+__device__ __forceinline__ double lane_xor(double v) {
+  const long long b = __double_as_longlong(v);
+  const int lo = lane_xor_i32<X>(static_cast<int>(b));
+  const int hi = lane_xor_i32<X>(static_cast<int>(b >> 32));
+  return __longlong_as_double((static_cast<long long>(hi) << 32) | static_cast<unsigned int>(lo));
+}
+
+template <int X, typename Acc>
+__device__ __forceinline__ void butterfly_lanes(Acc* v, int lane) {
+  const bool upper = (lane & X) != 0;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const Acc o = lane_xor<X>(v[r]);
+    v[r] = upper ? o - v[r] : v[r] + o;
+  }
+}
+
+// v H over N columns, 16 a lane
+template <int N, typename Acc>
+__device__ __forceinline__ void fwht_lanes(Acc* v, int lane) {
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if (r & h) continue;
+      const Acc a = v[r], c = v[r + h];
+      v[r] = a + c;
+      v[r + h] = a - c;
+    }
+  if constexpr (N > 16) butterfly_lanes<1>(v, lane);
+  if constexpr (N > 32) butterfly_lanes<2>(v, lane);
+  if constexpr (N > 64) butterfly_lanes<4>(v, lane);
+  if constexpr (N > 128) butterfly_lanes<8>(v, lane);
+}
+
+template <int N, bool MAX>
+__device__ __forceinline__ float row_extreme(float m) {
+  auto pick = [](float a, float b) { return MAX ? fmaxf(a, b) : fminf(a, b); };
+  if constexpr (N > 16) m = pick(m, lane_xor<1>(m));
+  if constexpr (N > 32) m = pick(m, lane_xor<2>(m));
+  if constexpr (N > 64) m = pick(m, lane_xor<4>(m));
+  if constexpr (N > 128) m = pick(m, lane_xor<8>(m));
+  return m;
+}
+
+// floor(v / s + 1/2) exactly, for |v| up to about 2^8 s: rint(v * (1/s)) is
+// at most one off, and the residual v - q s is exact in one fma. (Its bits:
+// where |v| >= s both v and q s are multiples of ulp(s) and the difference is
+// at most about s; below, q is 0 or +-1 and the difference is exact as one of
+// two numbers within a factor of two of each other.) So the comparison with
+// s / 2 decides the rounding as infinite precision would, and equal inputs
+// give equal codes whatever computes them.
+__device__ __forceinline__ float round_half_up(float v, float s, float inv) {
+  float q = rintf(v * inv);
+  const float r = fmaf(-q, s, v), h = 0.5f * s;
+  if (r >= h) q += 1.f;
+  if (r < -h) q -= 1.f;
+  return q;
+}
+
+// Written per token: keys, then values, head by head (the order of x).
+// Bound by HBM: a row reads head_dim elements and writes head_dim * b / 8 + 8
+// bytes. The transform runs in fp64: a row's sums are then exact (16-bit
+// inputs whose exponents span less than 2^37), so v, its range and every code
+// do not depend on the order of the additions.
+template <int N, int BITS, typename TIn, bool ROT>
+__global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict__ k,
+                                                          const TIn* __restrict__ v, int64_t rows,
+                                                          const int32_t* __restrict__ slots,
+                                                          Cache c) {
+  constexpr int LPR = N / 16;                  // lanes per row
+  constexpr float QMAX = static_cast<float>((1 << BITS) - 1);
+  const int u = threadIdx.x % LPR;
+  // rows: [T][2][heads]
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
+  const bool live = row < rows;
+  const int64_t rr = live ? row : rows - 1;
+  const int64_t tp = rr / c.heads;
+  const int h = static_cast<int>(rr - tp * c.heads);
+  const int part = static_cast<int>(tp & 1);
+  const int64_t t = tp >> 1;
+  const int32_t slot = slots[t];
+  const bool stored = live && slot >= 0 && (slot >> c.lg_page) < c.n_pages;
+
+  float f[16];
+  {
+    const TIn* src = (part ? v : k) + (t * c.heads + h) * N + u * 16;
+    if constexpr (ROT) {
+      double a[16];
+      load16(src, a);
+      fwht_lanes<N>(a, u);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) f[r] = static_cast<float>(a[r] * (1.0 / N));
+    } else {
+      load16(src, f);
+    }
+  }
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    lo = fminf(lo, f[r]);
+    hi = fmaxf(hi, f[r]);
+  }
+  lo = row_extreme<N, false>(lo);
+  hi = row_extreme<N, true>(hi);
+  float s = (hi - lo) / QMAX;
+  const bool flat = !(s >= 1.17549435e-38f);   // a step below fp32's normal range holds nothing
+  if (flat) s = 0.f;
+  const float inv = flat ? 0.f : 1.f / s;
+  const float z = flat ? 0.f : round_half_up(-lo, s, inv);
+  uint32_t w[16 * BITS / 32];
+#pragma unroll
+  for (int i = 0; i < 16 * BITS / 32; ++i) w[i] = 0u;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const float q = flat ? 0.f : fminf(fmaxf(round_half_up(f[r], s, inv) + z, 0.f), QMAX);
+    w[r * BITS / 32] |= static_cast<uint32_t>(q) << (r * BITS % 32);
+  }
+  if (!stored) return;
+  const int64_t at = c.row(part, slot, h);
+  uint32_t* dst = c.codes + at * (N * BITS / 32) + u * (16 * BITS / 32);
+  if constexpr (BITS == 4) {
+    *reinterpret_cast<uint2*>(dst) = uint2{w[0], w[1]};
+  } else {
+    *reinterpret_cast<uint4*>(dst) = uint4{w[0], w[1], w[2], w[3]};
+  }
+  if (u == 0) {
+    c.scales[at] = s;
+    c.zeros[at] = z;
+  }
+}
+
+template <typename TOut>
+__device__ __forceinline__ void store16(TOut* dst, const float* f) {
+  if constexpr (sizeof(TOut) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<float4*>(dst)[i] = float4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = static_cast<uint32_t>(f32_to_bf16(f[2 * i])) |
+             (static_cast<uint32_t>(f32_to_bf16(f[2 * i + 1])) << 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      reinterpret_cast<uint4*>(dst)[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+  }
+}
+
+// Rows [T][2][heads] of the slots, dense; a token without a slot reads as
+// zeros. Bound by HBM's writes: head_dim elements out for head_dim * b / 8 + 8
+// bytes in.
+template <int N, int BITS, typename TOut, bool ROT>
+__global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
+                                                         const int32_t* __restrict__ slots,
+                                                         int64_t rows, TOut* __restrict__ k,
+                                                         TOut* __restrict__ v) {
+  constexpr int LPR = N / 16;
+  const int u = threadIdx.x % LPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
+  const bool live = row < rows;
+  const int64_t rr = live ? row : rows - 1;
+  const int64_t tp = rr / c.heads;
+  const int h = static_cast<int>(rr - tp * c.heads);
+  const int part = static_cast<int>(tp & 1);
+  const int64_t t = tp >> 1;
+  const int32_t slot = slots[t];
+  float f[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) f[r] = 0.f;
+  if (slot >= 0 && (slot >> c.lg_page) < c.n_pages) {
+    const int64_t at = c.row(part, slot, h);
+    const uint32_t* src = c.codes + at * (N * BITS / 32) + u * (16 * BITS / 32);
+    uint32_t w[16 * BITS / 32];
+    if constexpr (BITS == 4) {
+      const uint2 p = *reinterpret_cast<const uint2*>(src);
+      w[0] = p.x; w[1] = p.y;
+    } else {
+      const uint4 p = *reinterpret_cast<const uint4*>(src);
+      w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w;
+    }
+    const float s = c.scales[at], z = c.zeros[at];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const uint32_t q = (w[r * BITS / 32] >> (r * BITS % 32)) & ((1u << BITS) - 1u);
+      f[r] = (static_cast<float>(q) - z) * s;
+    }
+  }
+  // every lane of a row takes the same branch above, so the butterflies see whole rows
+  if constexpr (ROT) fwht_lanes<N>(f, u);
+  if (live) store16((part ? v : k) + (t * c.heads + h) * N + u * 16, f);
+}
+
+// One workgroup per (sequence, query head); tokens in tiles of 256, one a
+// thread for the scores, then the head's columns over the threads for the
+// values, with the running maximum and sum of the softmax.
+template <int N, int BITS, typename T>
+__global__ __launch_bounds__(256) void cache_attn_kernel(const T* __restrict__ q, Cache c,
+                                                         int q_heads,
+                                                         const int32_t* __restrict__ table,
+                                                         int width,
+                                                         const int32_t* __restrict__ lens,
+                                                         float scale, int rotate,
+                                                         T* __restrict__ out) {
+  constexpr int CPW = 32 / BITS;
+  constexpr int PARTS = 256 / N;       // token subsets the value sums are split over
+  __shared__ float qs[N], acc_s[256], red[256], ps[256];
+  __shared__ int64_t rows[256];
+  const int b = blockIdx.y, hq = blockIdx.x, tid = threadIdx.x;
+  const int h = hq / (q_heads / c.heads);
+  auto turn = [&](float* a) {          // a <- a H in LDS
+    for (int w = 1; w < N; w <<= 1) {
+      __syncthreads();
+      if (tid < N / 2) {
+        const int i = (tid / w) * 2 * w + tid % w;
+        const float x = a[i], y = a[i + w];
+        a[i] = x + y;
+        a[i + w] = x - y;
+      }
+    }
+    __syncthreads();
+  };
+  const int64_t qrow = static_cast<int64_t>(b) * q_heads + hq;
+  if (tid < N) qs[tid] = Elem<T>::ld(q, qrow * N + tid);
+  if (rotate) turn(qs);
+  __syncthreads();
+  int64_t len = lens[b];
+  if (len > (static_cast<int64_t>(width) << c.lg_page)) len = static_cast<int64_t>(width) << c.lg_page;
+  float m = -INFINITY, l = 0.f, acc = 0.f;
+  for (int64_t t0 = 0; t0 < len; t0 += 256) {
+    const int64_t t = t0 + tid;
+    float a = -INFINITY;
+    int64_t at = -1;
+    if (t < len) {
+      const int32_t pg = table[static_cast<int64_t>(b) * width + (t >> c.lg_page)];
+      if (pg >= 0 && pg < c.n_pages) {
+        at = c.row_in(0, pg, static_cast<int>(t & ((1 << c.lg_page) - 1)), h);
+        const uint32_t* w = c.codes + at * (N / CPW);
+        const float z = c.zeros[at];
+        float d = 0.f;
+        for (int i = 0; i < N / CPW; ++i)
+          for (int e = 0; e < CPW; ++e)
+            d += qs[i * CPW + e] *
+                 (static_cast<float>((w[i] >> (e * BITS)) & ((1u << BITS) - 1u)) - z);
+        a = d * c.scales[at] * scale;
+      }
+    }
+    rows[tid] = at;
+    red[tid] = a;
+    __syncthreads();
+    for (int w = 128; w > 0; w >>= 1) {
+      if (tid < w) red[tid] = fmaxf(red[tid], red[tid + w]);
+      __syncthreads();
+    }
+    const float mn = fmaxf(m, red[0]);
+    __syncthreads();
+    const float p = at >= 0 ? expf(a - mn) : 0.f;
+    ps[tid] = p;
+    red[tid] = p;
+    __syncthreads();
+    for (int w = 128; w > 0; w >>= 1) {
+      if (tid < w) red[tid] += red[tid + w];
+      __syncthreads();
+    }
+    const float keep = mn > -INFINITY ? expf(m - mn) : 1.f;
+    l = l * keep + red[0];
+    acc *= keep;
+    m = mn;
+    const int col = tid % N;
+    const int64_t vals = c.part_rows();
+    for (int i = tid / N; i < 256; i += PARTS) {
+      const int64_t r = rows[i];
+      if (r < 0) continue;
+      const int64_t vr = r + vals;
+      const uint32_t w = c.codes[vr * (N / CPW) + col / CPW];
+      const float x = static_cast<float>((w >> ((col % CPW) * BITS)) & ((1u << BITS) - 1u));
+      acc += ps[i] * ((x - c.zeros[vr]) * c.scales[vr]);
+    }
+    __syncthreads();
+  }
+  acc_s[tid] = acc;
+  __syncthreads();
+  if (tid < N) {
+    float o = 0.f;
+    for (int i = 0; i < PARTS; ++i) o += acc_s[i * N + tid];
+    qs[tid] = l > 0.f ? o / l : 0.f;
+  }
+  if (rotate) turn(qs);
+  __syncthreads();
+  if (tid < N) Elem<T>::st(out, qrow * N + tid, qs[tid]);
+}
+
+// Calls fn with the kernel's compile-time choices.
+template <typename Fn>
+hipError_t by_shape(int dim, int bits, Fn&& fn) {
+  using std::integral_constant;
+  if (bits == 4) {
+    if (dim == 64) return fn(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    if (dim == 128) return fn(integral_constant<int, 128>{}, integral_constant<int, 4>{});
+    if (dim == 256) return fn(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  } else if (bits == 8) {
+    if (dim == 64) return fn(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    if (dim == 128) return fn(integral_constant<int, 128>{}, integral_constant<int, 8>{});
+    if (dim == 256) return fn(integral_constant<int, 256>{}, integral_constant<int, 8>{});
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,
+                              const int32_t* slots, int rotate, const Cache& c, hipStream_t s) {
+  const int64_t rows = T * 2 * c.heads;
+  return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
+    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
+    const dim3 grid(static_cast<unsigned>((rows * (N / 16) + 255) / 256));
+    auto go = [&](auto kernel, auto* kk, auto* vv) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, kk, vv, rows, slots, c);
+      return hipGetLastError();
+    };
+    if (dt == Dt::F32) {
+      auto* kk = static_cast<const float*>(k);
+      auto* vv = static_cast<const float*>(v);
+      return rotate ? go(cache_write_kernel<N, BITS, float, true>, kk, vv)
+                    : go(cache_write_kernel<N, BITS, float, false>, kk, vv);
+    }
+    auto* kk = static_cast<const uint16_t*>(k);
+    auto* vv = static_cast<const uint16_t*>(v);
+    return rotate ? go(cache_write_kernel<N, BITS, uint16_t, true>, kk, vv)
+                  : go(cache_write_kernel<N, BITS, uint16_t, false>, kk, vv);
+  });
+}
+
+hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, int rotate, Dt dt,
+                             void* k, void* v, hipStream_t s) {
+  const int64_t rows = T * 2 * c.heads;
+  return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
+    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
+    const dim3 grid(static_cast<unsigned>((rows * (N / 16) + 255) / 256));
+    auto go = [&](auto kernel, auto* kk, auto* vv) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, c, slots, rows, kk, vv);
+      return hipGetLastError();
+    };
+    if (dt == Dt::F32) {
+      auto* kk = static_cast<float*>(k);
+      auto* vv = static_cast<float*>(v);
+      return rotate ? go(cache_read_kernel<N, BITS, float, true>, kk, vv)
+                    : go(cache_read_kernel<N, BITS, float, false>, kk, vv);
+    }
+    auto* kk = static_cast<uint16_t*>(k);
+    auto* vv = static_cast<uint16_t*>(v);
+    return rotate ? go(cache_read_kernel<N, BITS, uint16_t, true>, kk, vv)
+                  : go(cache_read_kernel<N, BITS, uint16_t, false>, kk, vv);
+  });
+}
+
+size_t cache_attn_scratch_bytes(int, int, int, int, int64_t) { return 0; }
+
+hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cache& c,
+                             const int32_t* table, int width, const int32_t* lens, float scale,
+                             int rotate, void* out, void*, hipStream_t s) {
+  return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
+    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
+    const dim3 grid(static_cast<unsigned>(q_heads), static_cast<unsigned>(B));
+    if (dt == Dt::F32)
+      hipLaunchKernelGGL((cache_attn_kernel<N, BITS, float>), grid, dim3(256), 0, s,
+                         static_cast<const float*>(q), c, q_heads, table, width, lens, scale,
+                         rotate, static_cast<float*>(out));
+    else
+      hipLaunchKernelGGL((cache_attn_kernel<N, BITS, uint16_t>), grid, dim3(256), 0, s,
+                         static_cast<const uint16_t*>(q), c, q_heads, table, width, lens, scale,
+                         rotate, static_cast<uint16_t*>(out));
+    return hipGetLastError();
+  });
+}
+
+}  // namespace qwha

@@ -80,6 +80,12 @@ hipError_t launch_merge(const int32_t* row_ptr, const int32_t* E, const float* c
 hipError_t launch_qgemm(const uint16_t* x, int64_t T, int K, int N, const QuantW& qw,
                         const float* add, uint16_t* y, hipStream_t s);
 
+// y = x W_Q^T + alpha z F^T for T <= 64 tokens (decode.hip); z fp32 [T][K], or
+// null without an adapter
+hipError_t launch_decode(const void* x, Dt dt, int T, int K, int N, const QuantW& qw,
+                         const float* z, const int32_t* row_ptr, const int32_t* E,
+                         const float* c, float alpha, void* y, hipStream_t s);
+
 // ---- materialize
 // nblk > 1: rows of nblk blocks of 2^log_n columns (block-diagonal transform)
 hipError_t launch_materialize(const int32_t* row_ptr, const int32_t* E, const float* c, int d_out,
