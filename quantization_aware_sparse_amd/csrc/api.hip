@@ -594,7 +594,7 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
 
 size_t qwha_layer_decode_workspace_bytes(int64_t T, int32_t d_in, int32_t d_out, int64_t p) {
   if (T < 0 || T > QWHA_DECODE_MAX_T || d_in < 1 || d_out < 1 || p < 0) return 0;
-  return align256(static_cast<size_t>(T) * d_in * 4);
+  return align256(decode_scratch_bytes(T, d_in, p));
 }
 
 qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t d_in,
@@ -627,22 +627,17 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
   QWHA_NEED(x, 16);
   QWHA_NEED(y, 16);
   const size_t total = qwha_layer_decode_workspace_bytes(T, d_in, d_out, p);
-  if (workspace == nullptr || workspace_bytes < total)
-    return fail(QWHA_ERR_WORKSPACE, "layer decode workspace needs %zu bytes", total);
-  QWHA_NEED(workspace, 256);
-
-  float* z = nullptr;
-  if (p > 0) {
-    z = static_cast<float*>(workspace);
-    QWHA_TRY(hip_check(launch_fwht(x, static_cast<Dt>(act), z, Dt::F32, T * nblk, log_n,
-                                   1.0f / static_cast<float>(1 << log_n), 0, stream),
-                       "layer fwht"));
+  if (total > 0) {
+    if (workspace == nullptr || workspace_bytes < total)
+      return fail(QWHA_ERR_WORKSPACE, "layer decode workspace needs %zu bytes", total);
+    QWHA_NEED(workspace, 256);
   }
   const QuantW qw = make_quant(codes, scales, zeros, bits, group, d_in);
   return hip_check(timed(QWHA_KERNEL_LAYER_DECODE, stream,
                          [&] {
-                           return launch_decode(x, static_cast<Dt>(act), static_cast<int>(T), d_in,
-                                                d_out, qw, z, row_ptr, E, c, alpha, y, stream);
+                           return launch_decode(x, static_cast<Dt>(act), static_cast<int>(T),
+                                                log_n, nblk, d_out, qw, p, row_ptr, E, c, alpha, y,
+                                                workspace, stream);
                          }),
                    "layer decode");
 }

@@ -80,11 +80,12 @@ hipError_t launch_merge(const int32_t* row_ptr, const int32_t* E, const float* c
 hipError_t launch_qgemm(const uint16_t* x, int64_t T, int K, int N, const QuantW& qw,
                         const float* add, uint16_t* y, hipStream_t s);
 
-// y = x W_Q^T + alpha z F^T for T <= 64 tokens (decode.hip); z fp32 [T][K], or
-// null without an adapter
-hipError_t launch_decode(const void* x, Dt dt, int T, int K, int N, const QuantW& qw,
-                         const float* z, const int32_t* row_ptr, const int32_t* E,
-                         const float* c, float alpha, void* y, hipStream_t s);
+// y = x W_Q^T + alpha z F^T for T <= 64 tokens of K = nblk * 2^log_n columns
+// (decode.hip); p = 0: no adapter, row_ptr, E, c and scratch are not used
+size_t decode_scratch_bytes(int64_t T, int K, int64_t p);
+hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N,
+                         const QuantW& qw, int64_t p, const int32_t* row_ptr, const int32_t* E,
+                         const float* c, float alpha, void* y, void* scratch, hipStream_t s);
 
 // ---- materialize
 // nblk > 1: rows of nblk blocks of 2^log_n columns (block-diagonal transform)
