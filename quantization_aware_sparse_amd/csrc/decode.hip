@@ -175,88 +175,141 @@ struct Codes<8, S> {
   }
 };
 
-// ---- tokens as rows of the matrix instruction: lane l supplies row l % 16
+// ---- tokens as rows of the matrix instruction, staged by each wave for itself
+// in LDS: 128-byte lines in, operands out. A chunk is 32 S columns of 16 rows;
+// 16-byte piece p of row m lies at piece p ^ (m % pieces) of its row, so that
+// the rows one read covers hit distinct banks.
 template <typename T>
 struct Rows;
 template <>
 struct Rows<uint16_t> {
   static constexpr int TOK = 16;     // tokens per 16 rows
-  uint4 v;
-  __device__ __forceinline__ void load(const uint16_t* x, int64_t at, bool live) {
-    v = live ? *reinterpret_cast<const uint4*>(x + at) : uint4{0u, 0u, 0u, 0u};
-  }
-  __device__ __forceinline__ bf16x8 operand(int) const {
-    bf16x8 r;
-    __builtin_memcpy(&r, &v, 16);
-    return r;
-  }
 };
-// Rows 4i .. 4i + 2 are a token's upper, middle and lower 8 bits of mantissa
-// (each what is left of x after the one before, cut to bf16: exact), row
-// 4i + 3 is zero. The three results of a token lie in one lane.
+// fp32 tokens: rows 4i .. 4i + 2 are a token's upper, middle and lower 8 bits
+// of mantissa (each what is left of x after the one before, cut to bf16:
+// exact), row 4i + 3 is zero. The three results of a token lie in one lane.
 template <>
 struct Rows<float> {
   static constexpr int TOK = 4;
-  float4 v[2];
-  __device__ __forceinline__ void load(const float* x, int64_t at, bool live) {
-    const float4 zero = float4{0.f, 0.f, 0.f, 0.f};
-    v[0] = live ? reinterpret_cast<const float4*>(x + at)[0] : zero;
-    v[1] = live ? reinterpret_cast<const float4*>(x + at)[1] : zero;
-  }
-  __device__ __forceinline__ bf16x8 operand(int lane) const {
-    const int part = lane & 3;
-    const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-    uint32_t h[8], d[4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t a = __float_as_uint(f[i]) & 0xFFFF0000u;
-      const float r1 = f[i] - __uint_as_float(a);
-      const uint32_t b = __float_as_uint(r1) & 0xFFFF0000u;
-      const uint32_t c = __float_as_uint(r1 - __uint_as_float(b));
-      h[i] = part == 0 ? a : part == 1 ? b : part == 2 ? c : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_perm(h[2 * i + 1], h[2 * i], 0x07060302u);
-    bf16x8 r;
-    __builtin_memcpy(&r, d, 16);
-    return r;
+};
+
+template <int S>
+struct Stage {
+  static constexpr int PIECES = 4 * S;                 // of 16 bytes, per row
+  static constexpr int WORDS = 16 * 16 * S;            // of 4 bytes, per 16 rows
+  static __device__ __forceinline__ int at(int row, int piece) {
+    return (row * PIECES + (piece ^ (row % PIECES))) * 4;
   }
 };
 
-// ---- the transform of the tokens, zt[column][tp] fp32
-template <int LOG_N, typename TIn, int TT>
-__global__ __launch_bounds__((Fwht<LOG_N>::TPR > 256 ? Fwht<LOG_N>::TPR : 256)) void
-decode_fwht_kernel(const TIn* __restrict__ x, int tokens, int nblk, int tp,
-                   float* __restrict__ zt) {
-  using F = Fwht<LOG_N>;
-  constexpr int BLOCK = F::TPR > 256 ? F::TPR : 256, RPW = BLOCK / F::TPR;
-  __shared__ float lds_all[RPW * F::LDS];
-  const int slot = threadIdx.x / F::TPR, u = threadIdx.x % F::TPR;
-  const int blk = blockIdx.x * RPW + slot, t0 = blockIdx.y * TT;
-  const bool live = blk < nblk;
-  const int64_t K = static_cast<int64_t>(nblk) << LOG_N;
-  float v[TT][F::EPT];
+// A wave's part of a chunk on its way from memory to LDS.
+template <int S, typename T>
+struct Incoming;
+template <int S>
+struct Incoming<S, uint16_t> {
+  uint4 v[S];
+  __device__ __forceinline__ void load(const uint16_t* x, int64_t K, int t0, int tokens, int col,
+                                       int lane) {
 #pragma unroll
-  for (int i = 0; i < TT; ++i) {
-    if (live && t0 + i < tokens) {
-      load16(x + (t0 + i) * K + (static_cast<int64_t>(blk) << LOG_N) + u * 16, v[i]);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) v[i][r] = 0.f;
+    for (int i = 0; i < S; ++i) {
+      const int e = i * 64 + lane, row = e / (4 * S), piece = e % (4 * S);
+      v[i] = t0 + row < tokens
+                 ? *reinterpret_cast<const uint4*>(x + (t0 + row) * K + col + 8 * piece)
+                 : uint4{0u, 0u, 0u, 0u};
     }
   }
+  __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
 #pragma unroll
-  for (int i = 0; i < TT; ++i) F::run(v[i], lds_all + slot * F::LDS, u);
-  if (!live) return;
+    for (int i = 0; i < S; ++i) {
+      const int e = i * 64 + lane;
+      *reinterpret_cast<uint4*>(lds + Stage<S>::at(e / (4 * S), e % (4 * S))) = v[i];
+    }
+  }
+};
+template <int S>
+struct Incoming<S, float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float* x, int64_t K, int t0, int tokens, int col,
+                                       int lane) {
+    const int tok = lane / (4 * S), piece = lane % (4 * S);   // lanes past 16 S have no piece
+    const bool live = tok < 4 && t0 + tok < tokens;
+    const float4* p = reinterpret_cast<const float4*>(x + (live ? (t0 + tok) * K + col + 8 * piece : 0));
+    const float4 zero = float4{0.f, 0.f, 0.f, 0.f};
+    v[0] = live ? p[0] : zero;
+    v[1] = live ? p[1] : zero;
+  }
+  __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
+    const int tok = lane / (4 * S), piece = lane % (4 * S);
+    const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t h[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[0][i] = __float_as_uint(f[i]);
+      const float r1 = f[i] - __uint_as_float(h[0][i] & 0xFFFF0000u);
+      h[1][i] = __float_as_uint(r1);
+      h[2][i] = __float_as_uint(r1 - __uint_as_float(h[1][i] & 0xFFFF0000u));
+    }
+    if (tok < 4) {
+#pragma unroll
+      for (int part = 0; part < 4; ++part) {
+        uint32_t d[4] = {0u, 0u, 0u, 0u};
+        if (part < 3)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            d[i] = __builtin_amdgcn_perm(h[part][2 * i + 1], h[part][2 * i], 0x07060302u);
+        *reinterpret_cast<uint4*>(lds + Stage<S>::at(4 * tok + part, piece)) =
+            uint4{d[0], d[1], d[2], d[3]};
+      }
+    }
+  }
+};
+
+// ---- the transform of the tokens, zt[column][tp] fp32: four tokens of a
+// block side by side in a workgroup, so that a column's values leave together
+template <int LOG_N>
+struct Zt {
+  using F = Fwht<LOG_N>;
+  static constexpr int TT = LOG_N <= 12 ? 4 : LOG_N == 13 ? 2 : 1;     // tokens side by side
+  static constexpr int BLOCK = F::TPR * TT > 256 ? F::TPR * TT : 256;
+  static constexpr int BLKS = BLOCK / (F::TPR * TT);                   // blocks of columns
+};
+template <int LOG_N, typename TIn>
+__global__ __launch_bounds__(Zt<LOG_N>::BLOCK) void decode_fwht_kernel(const TIn* __restrict__ x,
+                                                                       int tokens, int nblk,
+                                                                       int tp,
+                                                                       float* __restrict__ zt) {
+  using F = Fwht<LOG_N>;
+  using Z = Zt<LOG_N>;
+  __shared__ float lds_all[Z::BLKS * Z::TT * F::LDS];
+  const int slot = threadIdx.x / F::TPR, u = threadIdx.x % F::TPR;
+  const int blk = blockIdx.x * Z::BLKS + slot / Z::TT, t = blockIdx.y * Z::TT + slot % Z::TT;
+  const int64_t K = static_cast<int64_t>(nblk) << LOG_N;
+  float* lds = lds_all + slot * F::LDS;
+  float v[16];
+  if (blk < nblk && t < tokens) {
+    load16(x + t * K + (static_cast<int64_t>(blk) << LOG_N) + u * 16, v);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[r] = 0.f;
+  }
+  F::run(v, lds, u);
   constexpr float scale = 1.f / static_cast<float>(F::N);
+  __syncthreads();
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    float* dst = zt + ((static_cast<int64_t>(blk) << LOG_N) + F::out_index(u, r)) * tp + t0;
-    if constexpr (TT == 4) {
+  for (int r = 0; r < 16; ++r) lds[F::pad(F::out_index(u, r))] = v[r] * scale;
+  __syncthreads();
+  const int b0 = blockIdx.x * Z::BLKS, t0 = blockIdx.y * Z::TT;
+  for (int e = threadIdx.x; e < Z::BLKS * F::N; e += Z::BLOCK) {
+    const int bl = e >> LOG_N, j = e & (F::N - 1);
+    if (b0 + bl >= nblk) break;
+    const float* src = lds_all + bl * Z::TT * F::LDS + F::pad(j);
+    float* dst = zt + ((static_cast<int64_t>(b0 + bl) << LOG_N) + j) * tp + t0;
+    if constexpr (Z::TT == 4) {
       *reinterpret_cast<float4*>(dst) =
-          float4{v[0][r] * scale, v[1][r] * scale, v[2][r] * scale, v[3][r] * scale};
+          float4{src[0], src[F::LDS], src[2 * F::LDS], src[3 * F::LDS]};
     } else {
-      dst[0] = v[0][r] * scale;
+#pragma unroll
+      for (int i = 0; i < Z::TT; ++i) dst[i] = src[i * F::LDS];
     }
   }
 }
@@ -269,6 +322,9 @@ decode_fwht_kernel(const TIn* __restrict__ x, int tokens, int nblk, int tp,
 // chunk, so a lane reads consecutive bytes of a row of codes and a chunk never
 // crosses a group (32 S <= group). Results: lane l has W's row l % 16 and the
 // token rows 4 (l / 16) .. + 4.
+// The nonzeros of the same rows of F lie side by side in E and c: the first
+// kEntries of them are fetched beside the codes and wait in LDS, so that only
+// the gather of z is left behind the product.
 struct DecodeArgs {
   int tokens, K, N, tp;
   QuantW qw;
@@ -279,19 +335,35 @@ struct DecodeArgs {
   float alpha;
 };
 
+constexpr int kThreads = kDecodeWaves * 64;
+constexpr int kEntries = 4 * kThreads;   // nonzeros staged at a time
+
 template <int BITS, int S, int MT, int NT, typename T>
-__global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(const T* __restrict__ x,
-                                                                   DecodeArgs a,
-                                                                   T* __restrict__ y) {
+__global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ x, DecodeArgs a,
+                                                          T* __restrict__ y) {
   constexpr int TB = Rows<T>::TOK * MT;              // tokens of the workgroup
   constexpr int U = 16 / S / MT > 0 ? 16 / S / MT : 1;
   constexpr int LD = 16 * NT + 1;
-  __shared__ float red[kDecodeWaves][TB][LD];
+  constexpr int RPW = 2 * NT;                        // rows of F per wave
+  constexpr int XW = MT * Stage<S>::WORDS;           // staged words of a wave
+  constexpr int RW = TB * LD;                        // words of a wave's sums
+  // a wave's staged tokens and, later, its sums share their place
+  constexpr int WAVE = (XW > RW ? XW : RW) + 3 & ~3;
+  __shared__ __attribute__((aligned(16))) uint32_t own[kDecodeWaves][WAVE];
   __shared__ float ad[16 * NT][TB + 4];
+  __shared__ uint2 ent[kEntries];                    // column, value
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int lr = lane & 15, lq = lane >> 4;
   const int n0 = blockIdx.x * 16 * NT, t0 = blockIdx.y * TB;
   const int nchunks = a.K / (32 * S);
+
+  int rp[RPW + 1], k0 = 0, kend = 0;
+  if (a.zt != nullptr) {
+    k0 = a.row_ptr[n0];
+    kend = a.row_ptr[min(n0 + 16 * NT, a.N)];
+#pragma unroll
+    for (int i = 0; i <= RPW; ++i) rp[i] = a.row_ptr[min(n0 + w * RPW + i, a.N)];
+  }
 
   const uint32_t* crow[NT];
   const float *srow[NT], *zrow[NT];
@@ -301,14 +373,6 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(const T* __re
     crow[j] = a.qw.codes + n * a.qw.wpr;
     srow[j] = a.qw.scales + n * a.qw.gpr;
     zrow[j] = a.qw.zeros + n * a.qw.gpr;
-  }
-  int64_t xat[MT];
-  bool xlive[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int t = t0 + i * Rows<T>::TOK + lr / (16 / Rows<T>::TOK);
-    xlive[i] = t < a.tokens && (sizeof(T) == 2 || (lr & 3) != 3);
-    xat[i] = xlive[i] ? static_cast<int64_t>(t) * a.K : 0;
   }
   bf16x8 ones;
   {
@@ -322,9 +386,11 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(const T* __re
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = zero4;
 
-  for (int c0 = w; c0 < nchunks; c0 += kDecodeWaves * U) {
+  uint2 en[4];
+  bool first = true;
+  for (int c0 = w; c0 < nchunks || first; c0 += kDecodeWaves * U) {
     Codes<BITS, S> cw[U][NT];
-    Rows<T> xr[U][S][MT];
+    Incoming<S, T> xr[U][MT];
     float sc[U][NT], zo[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -338,20 +404,30 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(const T* __re
       }
 #pragma unroll
       for (int i = 0; i < MT; ++i)
+        xr[u][i].load(x, a.K, t0 + i * Rows<T>::TOK, a.tokens, col, lane);
+    }
+    if (first) {
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-          xr[u][s][i].load(x, xat[i] + col + 8 * S * lq + 8 * s, xlive[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int64_t k = static_cast<int64_t>(k0) + i * kThreads + threadIdx.x;
+        if (k < kend) en[i] = uint2{static_cast<uint32_t>(a.E[2 * k + 1]), __float_as_uint(a.c[k])};
+      }
+      first = false;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (c0 + u * kDecodeWaves >= nchunks) break;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) xr[u][i].store(&own[w][i * Stage<S>::WORDS], lane);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       f32x4 g[MT][NT], xs[MT];
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         bf16x8 xf[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          xf[i] = xr[u][s][i].operand(lane);
+          xf[i] = *reinterpret_cast<const bf16x8*>(
+              &own[w][i * Stage<S>::WORDS + Stage<S>::at(lr, lq * S + s)]);
           xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], ones, s ? xs[i] : zero4, 0, 0, 0);
         }
 #pragma unroll
@@ -362,6 +438,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(const T* __re
             g[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf, s ? g[i][j] : zero4, 0, 0, 0);
         }
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const float z = Codes<BITS, S>::OFF + zo[u][j];
@@ -373,54 +450,76 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void decode_kernel(const T* __re
       }
     }
   }
+  float* red = reinterpret_cast<float*>(own[w]);
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) red[w][i * 16 + 4 * lq + r][j * 16 + lr] = acc[i][j][r];
+        for (int r = 0; r < 4; ++r) red[(i * 16 + 4 * lq + r) * LD + j * 16 + lr] = acc[i][j][r];
       } else {
-        red[w][i * 4 + lq][j * 16 + lr] = acc[i][j][0] + acc[i][j][1] + acc[i][j][2];
+        red[(i * 4 + lq) * LD + j * 16 + lr] = acc[i][j][0] + acc[i][j][1] + acc[i][j][2];
       }
     }
 
-  // the nonzeros of these rows of F, a wave a row: TB / 4 lanes hold 4 tokens
-  // each of one nonzero's column
-  constexpr int LPN = TB / 4, NPW = 64 / LPN;
+  // the nonzeros, a wave RPW rows: lpn lanes hold 4 tokens each of one
+  // nonzero's column
   if (a.zt != nullptr) {
-    const int sub = lane / LPN;
-    const float* zl = a.zt + t0 + (lane % LPN) * 4;
-    for (int i = w; i < 16 * NT; i += kDecodeWaves) {
-      f32x4 s4 = zero4;
-      if (n0 + i < a.N) {
-        const int k1 = a.row_ptr[n0 + i + 1];
-        for (int k = a.row_ptr[n0 + i] + sub; k < k1; k += NPW) {
-          const int64_t j = a.E[2 * static_cast<int64_t>(k) + 1];
-          const f32x4 zv = *reinterpret_cast<const f32x4*>(zl + j * a.tp);
-          const float cv = a.c[k];
+    const int lpn = min(a.tp, TB) / 4, npw = 64 / lpn;
+    const int sub = lane / lpn;
+    const float* zl = a.zt + t0 + (lane % lpn) * 4;
+    f32x4 s4[RPW];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s4[r] = fmaf(cv, zv[r], s4[r]);
+    for (int i = 0; i < RPW; ++i) s4[i] = zero4;
+    for (int kb = k0;;) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * kThreads + static_cast<int>(threadIdx.x) < kend - kb)
+          ent[i * kThreads + threadIdx.x] = en[i];
+      __syncthreads();
+      const int held = min(kend - kb, kEntries);
+#pragma unroll
+      for (int i = 0; i < RPW; ++i) {
+        const int e1 = min(rp[i + 1] - kb, held);
+#pragma unroll 4
+        for (int k = max(rp[i] - kb, 0) + sub; k < e1; k += npw) {
+          const uint2 e = ent[k];
+          const f32x4 zv = *reinterpret_cast<const f32x4*>(zl + static_cast<int64_t>(e.x) * a.tp);
+          const float cv = __uint_as_float(e.y);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s4[i][r] = fmaf(cv, zv[r], s4[i][r]);
         }
       }
+      if (held == kend - kb) break;
+      kb += held;
+      __syncthreads();
 #pragma unroll
-      for (int o = LPN; o < 64; o <<= 1)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s4[r] += __shfl_xor(s4[r], o);
-      if (lane < LPN)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ad[i][lane * 4 + r] = s4[r];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t k = static_cast<int64_t>(kb) + i * kThreads + threadIdx.x;
+        if (k < kend) en[i] = uint2{static_cast<uint32_t>(a.E[2 * k + 1]), __float_as_uint(a.c[k])};
+      }
     }
+    for (int o = lpn; o < 64; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < RPW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s4[i][r] += __shfl_xor(s4[i][r], o);
+    if (lane < lpn)
+#pragma unroll
+      for (int i = 0; i < RPW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ad[w * RPW + i][lane * 4 + r] = s4[i][r];
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < TB * 16 * NT; e += kDecodeWaves * 64) {
+  for (int e = threadIdx.x; e < TB * 16 * NT; e += kThreads) {
     const int t = e / (16 * NT), n = e % (16 * NT);
+    if (t0 + t >= a.tokens || n0 + n >= a.N) continue;
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < kDecodeWaves; ++i) v += red[i][t][n];
+    for (int i = 0; i < kDecodeWaves; ++i) v += __uint_as_float(own[i][t * LD + n]);
     if (a.zt != nullptr) v = fmaf(a.alpha, ad[n][t], v);
-    if (t0 + t < a.tokens && n0 + n < a.N)
-      Elem<T>::st(y, static_cast<int64_t>(t0 + t) * a.N + n0 + n, v);
+    Elem<T>::st(y, static_cast<int64_t>(t0 + t) * a.N + n0 + n, v);
   }
 }
 
@@ -436,7 +535,9 @@ hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
 template <int BITS, int S, typename T>
 hipError_t decode_s(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   const int tiles = (a.tokens + Rows<T>::TOK - 1) / Rows<T>::TOK;
-  if (tiles == 1) return decode_t<BITS, S, 1, 1, T>(x, a, y, s);
+  if (tiles == 1)
+    return a.N >= 8192 ? decode_t<BITS, S, 1, 2, T>(x, a, y, s)
+                       : decode_t<BITS, S, 1, 1, T>(x, a, y, s);
   if (tiles == 2) return decode_t<BITS, S, 2, 1, T>(x, a, y, s);
   return decode_t<BITS, S, 4, 1, T>(x, a, y, s);
 }
@@ -461,15 +562,10 @@ hipError_t decode_d(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
 
 template <int LOG_N, typename T>
 hipError_t fwht_t(const T* x, int tokens, int nblk, int tp, float* zt, hipStream_t s) {
-  using F = Fwht<LOG_N>;
-  constexpr int BLOCK = F::TPR > 256 ? F::TPR : 256, RPW = BLOCK / F::TPR;
-  const int gx = (nblk + RPW - 1) / RPW;
-  if (tokens > 1)
-    hipLaunchKernelGGL((decode_fwht_kernel<LOG_N, T, 4>), dim3(gx, (tokens + 3) / 4), dim3(BLOCK),
-                       0, s, x, tokens, nblk, tp, zt);
-  else
-    hipLaunchKernelGGL((decode_fwht_kernel<LOG_N, T, 1>), dim3(gx, 1), dim3(BLOCK), 0, s, x,
-                       tokens, nblk, tp, zt);
+  using Z = Zt<LOG_N>;
+  const dim3 grid((nblk + Z::BLKS - 1) / Z::BLKS, (tokens + Z::TT - 1) / Z::TT);
+  hipLaunchKernelGGL((decode_fwht_kernel<LOG_N, T>), grid, dim3(Z::BLOCK), 0, s, x, tokens, nblk,
+                     tp, zt);
   return hipGetLastError();
 }
 
@@ -487,8 +583,12 @@ hipError_t fwht_d(const T* x, int tokens, int log_n, int nblk, int tp, float* zt
   }
 }
 
-// tokens a column of zt holds: whole workgroup tiles
-int padded_tokens(int T) { return (T + 15) / 16 * 16 == 48 ? 64 : (T + 15) / 16 * 16; }
+// tokens a column of zt holds: a power of two, 4 at least
+int padded_tokens(int T) {
+  int tp = 4;
+  while (tp < T) tp *= 2;
+  return tp;
+}
 
 }  // namespace
 
