@@ -30,41 +30,59 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kDecodeWaves = 8;
 
-// (x & mask) | bits in one instruction
+// (x & mask) | bits in one instruction: the mask in a vector register (one
+// scalar operand per instruction), the bits a scalar
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  return (x & mask) | bits;
+  uint32_t d;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(x), "v"(mask), "s"(bits));
+  return d;
+}
+__device__ __forceinline__ uint32_t in_vgpr(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Loads from a base that is the same in the whole wave plus 32-bit offsets
+// (bytes) of the lanes: one address register a lane, none per load.
+template <typename V>
+__device__ __forceinline__ V ld_at(const void* base, uint32_t off) {
+  return *reinterpret_cast<const V*>(static_cast<const char*>(base) + off);
 }
 
 // ---- a lane's codes of a chunk: 8 S consecutive columns of one row, as S
-// operands of 8 columns each (bf16 of OFF + q, two to a word)
+// operands of 8 columns each (bf16 of OFF + q, two to a word). `base` is the
+// first row of the tile, `off` the lane's row in bytes, `col` the lane's first
+// column (chunk plus `part`); MASK selects a code in both halves of a word.
 template <int BITS, int S>
 struct Codes;
 
 template <int S>
 struct Codes<4, S> {
   static constexpr float OFF = 16.f;
+  static constexpr uint32_t MASK = 0x00780078u;
   uint32_t w[S];
-  __device__ __forceinline__ void load(const uint32_t* row, int col, int) {
-    const uint32_t* p = row + col / 8;
+  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
+                                       int) {
+    const uint32_t* b = base + chunk / 8;
+    const uint32_t o = off + part / 2;
     if constexpr (S == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      const uint4 v = ld_at<uint4>(b, o);
       w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
     } else if constexpr (S == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      const uint2 v = ld_at<uint2>(b, o);
       w[0] = v.x; w[1] = v.y;
     } else {
-      w[0] = *p;
+      w[0] = ld_at<uint32_t>(b, o);
     }
   }
   // bf16(16 + q) = 0x4180 | q << 3: low nibbles from w << 3, high ones from
   // w >> 1, a byte of each to a pair
-  __device__ __forceinline__ bf16x8 operand(int i) const {
+  __device__ __forceinline__ bf16x8 operand(int i, uint32_t mask) const {
     const uint32_t u = w[i] << 3, v = w[i] >> 1;
     uint32_t d[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      d[k] = and_or(__builtin_amdgcn_perm(v, u, 0x0C040C00u + 0x00010001u * k), 0x00780078u,
-                    0x41804180u);
+      d[k] = and_or(__builtin_amdgcn_perm(v, u, 0x0C040C00u + 0x00010001u * k), mask, 0x41804180u);
     bf16x8 r;
     __builtin_memcpy(&r, d, 16);
     return r;
@@ -74,27 +92,31 @@ struct Codes<4, S> {
 template <int S>
 struct Codes<2, S> {
   static constexpr float OFF = 4.f;
+  static constexpr uint32_t MASK = 0x00600060u;
   uint32_t w[S == 4 ? 2 : 1];
-  __device__ __forceinline__ void load(const uint32_t* row, int col, int) {
+  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
+                                       int) {
+    const uint32_t* b = base + chunk / 16;
+    const uint32_t o = off + part / 4;
     if constexpr (S == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(row + col / 16);
+      const uint2 v = ld_at<uint2>(b, o);
       w[0] = v.x; w[1] = v.y;
     } else if constexpr (S == 2) {
-      w[0] = row[col / 16];
+      w[0] = ld_at<uint32_t>(b, o);
     } else {
-      w[0] = reinterpret_cast<const uint16_t*>(row)[col / 8];
+      w[0] = ld_at<uint16_t>(b, o);
     }
   }
   // bf16(4 + q) = 0x4080 | q << 5
-  __device__ __forceinline__ bf16x8 operand(int i) const {
+  __device__ __forceinline__ bf16x8 operand(int i, uint32_t mask) const {
     const uint32_t x = w[i / 2] >> (16 * (i % 2));
     uint32_t d[4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       d[2 * k] = and_or(__builtin_amdgcn_perm(x << 3, x << 5, 0x0C040C00u + 0x00010001u * k),
-                        0x00600060u, 0x40804080u);
+                        mask, 0x40804080u);
       d[2 * k + 1] = and_or(__builtin_amdgcn_perm(x >> 1, x << 1, 0x0C040C00u + 0x00010001u * k),
-                            0x00600060u, 0x40804080u);
+                            mask, 0x40804080u);
     }
     bf16x8 r;
     __builtin_memcpy(&r, d, 16);
@@ -109,20 +131,22 @@ struct Codes<3, S> {
   static constexpr float OFF = 8.f;
   static constexpr int NW = S == 4 ? 5 : S == 2 ? 3 : 2;   // (9 + 8 S) / 10 words, rounded up
   static constexpr int NL = S == 4 ? 3 : S == 2 ? 2 : 1;   // 24 S bits
+  static constexpr uint32_t MASK = 0x00700070u;
   uint32_t w[NW];
   int sh;
-  __device__ __forceinline__ void load(const uint32_t* row, int col, int wpr) {
-    const int base = col / 10;
-    sh = 3 * (col - 10 * base);
+  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
+                                       int wpr) {
+    const int col = chunk + part, word = col / 10;
+    sh = 3 * (col - 10 * word);
 #pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = row[min(base + i, wpr - 1)];
+    for (int i = 0; i < NW; ++i) w[i] = ld_at<uint32_t>(base, off + 4 * min(word + i, wpr - 1));
   }
   __device__ __forceinline__ uint32_t limb(int i) const {
     const uint32_t lo = (i < NW ? w[i] & 0x3FFFFFFFu : 0u) >> (2 * i);
     return lo | (i + 1 < NW ? w[i + 1] << (30 - 2 * i) : 0u);
   }
   // bf16(8 + q) = 0x4100 | q << 4
-  __device__ __forceinline__ bf16x8 operand(int i) const {
+  __device__ __forceinline__ bf16x8 operand(int i, uint32_t mask) const {
     uint32_t m[NL + 1];
 #pragma unroll
     for (int k = 0; k < NL; ++k) m[k] = __builtin_amdgcn_alignbit(limb(k + 1), limb(k), sh);
@@ -134,7 +158,7 @@ struct Codes<3, S> {
       const uint32_t t =
           __builtin_amdgcn_alignbit(m[bit / 32 + 1 < NL ? bit / 32 + 1 : NL], m[bit / 32], bit % 32) &
           63u;
-      d[k] = and_or((t << 4) | (t << 17), 0x00700070u, 0x41004100u);
+      d[k] = and_or((t << 4) | (t << 17), mask, 0x41004100u);
     }
     bf16x8 r;
     __builtin_memcpy(&r, d, 16);
@@ -145,22 +169,25 @@ struct Codes<3, S> {
 template <int S>
 struct Codes<8, S> {
   static constexpr float OFF = 0.f;
+  static constexpr uint32_t MASK = 0u;
   uint32_t w[2 * S];
-  __device__ __forceinline__ void load(const uint32_t* row, int col, int) {
-    const uint32_t* p = row + col / 4;
+  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
+                                       int) {
+    const uint32_t* b = base + chunk / 4;
+    const uint32_t o = off + part;
     if constexpr (S == 1) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      const uint2 v = ld_at<uint2>(b, o);
       w[0] = v.x; w[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < S / 2; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        const uint4 v = ld_at<uint4>(b, o + 16 * i);
         w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
       }
     }
   }
   // the upper halves of fp32(q): exact, q < 2^8
-  __device__ __forceinline__ bf16x8 operand(int i) const {
+  __device__ __forceinline__ bf16x8 operand(int i, uint32_t) const {
     uint32_t d[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -202,21 +229,25 @@ struct Stage {
   }
 };
 
-// A wave's part of a chunk on its way from memory to LDS.
+// A wave's part of a chunk on its way from memory to LDS. Rows past the last
+// token repeat it (their results are not stored).
 template <int S, typename T>
 struct Incoming;
 template <int S>
 struct Incoming<S, uint16_t> {
   uint4 v[S];
-  __device__ __forceinline__ void load(const uint16_t* x, int64_t K, int t0, int tokens, int col,
-                                       int lane) {
+  // byte offsets of a lane's pieces in x
+  static __device__ __forceinline__ void offsets(uint32_t* off, int K, int t0, int tokens,
+                                                 int lane) {
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int e = i * 64 + lane, row = e / (4 * S), piece = e % (4 * S);
-      v[i] = t0 + row < tokens
-                 ? *reinterpret_cast<const uint4*>(x + (t0 + row) * K + col + 8 * piece)
-                 : uint4{0u, 0u, 0u, 0u};
+      const int e = i * 64 + lane;
+      off[i] = 2 * (min(t0 + e / (4 * S), tokens - 1) * K + 8 * (e % (4 * S)));
     }
+  }
+  __device__ __forceinline__ void load(const uint16_t* x, const uint32_t* off) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) v[i] = ld_at<uint4>(x, off[i]);
   }
   __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
 #pragma unroll
@@ -229,14 +260,14 @@ struct Incoming<S, uint16_t> {
 template <int S>
 struct Incoming<S, float> {
   float4 v[2];
-  __device__ __forceinline__ void load(const float* x, int64_t K, int t0, int tokens, int col,
-                                       int lane) {
-    const int tok = lane / (4 * S), piece = lane % (4 * S);   // lanes past 16 S have no piece
-    const bool live = tok < 4 && t0 + tok < tokens;
-    const float4* p = reinterpret_cast<const float4*>(x + (live ? (t0 + tok) * K + col + 8 * piece : 0));
-    const float4 zero = float4{0.f, 0.f, 0.f, 0.f};
-    v[0] = live ? p[0] : zero;
-    v[1] = live ? p[1] : zero;
+  static __device__ __forceinline__ void offsets(uint32_t* off, int K, int t0, int tokens,
+                                                 int lane) {
+    // lanes past 16 S have no piece of their own
+    off[0] = 4 * (min(t0 + lane / (4 * S), tokens - 1) * K + 8 * (lane % (4 * S)));
+  }
+  __device__ __forceinline__ void load(const float* x, const uint32_t* off) {
+    v[0] = ld_at<float4>(x, off[0]);
+    v[1] = ld_at<float4>(x, off[0] + 16);
   }
   __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
     const int tok = lane / (4 * S), piece = lane % (4 * S);
@@ -325,60 +356,117 @@ __global__ __launch_bounds__(Zt<LOG_N>::BLOCK) void decode_fwht_kernel(const TIn
 // The nonzeros of the same rows of F lie side by side in E and c: the first
 // kEntries of them are fetched beside the codes and wait in LDS, so that only
 // the gather of z is left behind the product.
+// With few tokens every workgroup transforms them itself, in LDS, while its
+// codes are on their way (LOCAL): one launch, and no way through memory for z.
+// The code is kept short (loops, no peeled copies): a workgroup runs through
+// most of it once, and fetching instructions costs as much as fetching codes.
 struct DecodeArgs {
   int tokens, K, N, tp;
   QuantW qw;
-  const float* zt;             // null without an adapter
-  const int32_t* row_ptr;
+  const float* zt;             // zt[column][tp], unless LOCAL or p = 0
+  const int32_t* row_ptr;      // null without an adapter
   const int32_t* E;
   const float* c;
-  float alpha;
+  float alpha;                 // LOCAL: alpha / b, for the plain sums of the transform
+  int log_b;
 };
 
 constexpr int kThreads = kDecodeWaves * 64;
 constexpr int kEntries = 4 * kThreads;   // nonzeros staged at a time
+constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
+constexpr int kLocalTokens = 4;
 
-template <int BITS, int S, int MT, int NT, typename T>
+__device__ __forceinline__ int zpad(int j) { return j + (j >> 4); }
+
+// z <- x H per block of 2^log_b columns, z[t * zld + zpad(column)], unscaled:
+// passes of 4 index bits, 16 values a thread, in place.
+template <typename T>
+__device__ __forceinline__ void local_transform(const T* __restrict__ x, int tokens, int K,
+                                                int log_b, int zld, float* z) {
+  const int per = K >> 4, items = tokens * per;
+  int done = 0;                              // index bits done
+#pragma unroll 1
+  for (int lo = 0; done < log_b; lo = min(lo + 4, log_b - 4)) {
+    const int hi = lo + 4;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < items; e += kThreads) {
+      const int t = e / per, u = e - t * per;
+      const int j0 = (u & ((1 << lo) - 1)) | ((u >> lo) << hi);
+      float* zr = z + t * zld;
+      float v[16];
+      if (done == 0) {
+        load16(x + static_cast<int64_t>(t) * K + u * 16, v);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = zr[zpad(j0 + (r << lo))];
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (lo + b < done) continue;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if (r & (1 << b)) continue;
+          const float p = v[r], q = v[r + (1 << b)];
+          v[r] = p + q;
+          v[r + (1 << b)] = p - q;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) zr[zpad(j0 + (r << lo))] = v[r];
+    }
+    done = hi;
+    __syncthreads();
+  }
+}
+
+template <int BITS, int S, int MT, int NT, typename T, bool LOCAL>
 __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ x, DecodeArgs a,
                                                           T* __restrict__ y) {
   constexpr int TB = Rows<T>::TOK * MT;              // tokens of the workgroup
-  constexpr int U = 16 / S / MT > 0 ? 16 / S / MT : 1;
+  constexpr int U = 16 / S / MT > 0 ? (16 / S / MT > 4 ? 4 : 16 / S / MT) : 1;
   constexpr int LD = 16 * NT + 1;
   constexpr int RPW = 2 * NT;                        // rows of F per wave
   constexpr int XW = MT * Stage<S>::WORDS;           // staged words of a wave
   constexpr int RW = TB * LD;                        // words of a wave's sums
   // a wave's staged tokens and, later, its sums share their place
-  constexpr int WAVE = (XW > RW ? XW : RW) + 3 & ~3;
+  constexpr int WAVE = ((XW > RW ? XW : RW) + 3) & ~3;
+  constexpr int XO = sizeof(T) == 2 ? S : 1;
+  using Code = Codes<BITS, S>;
   __shared__ __attribute__((aligned(16))) uint32_t own[kDecodeWaves][WAVE];
-  __shared__ float ad[16 * NT][TB + 4];
+  __shared__ float ad[16 * NT][LOCAL ? 4 : TB + 4];
   __shared__ uint2 ent[kEntries];                    // column, value
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  extern __shared__ float zl[];                      // LOCAL: [tokens][zpad(K)]
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int n0 = blockIdx.x * 16 * NT, t0 = blockIdx.y * TB;
   const int nchunks = a.K / (32 * S);
+  const bool adapter = a.row_ptr != nullptr;
 
-  int rp[RPW + 1], k0 = 0, kend = 0;
-  if (a.zt != nullptr) {
+  int k0 = 0, kend = 0;
+  if (adapter) {
     k0 = a.row_ptr[n0];
     kend = a.row_ptr[min(n0 + 16 * NT, a.N)];
-#pragma unroll
-    for (int i = 0; i <= RPW; ++i) rp[i] = a.row_ptr[min(n0 + w * RPW + i, a.N)];
   }
-
-  const uint32_t* crow[NT];
-  const float *srow[NT], *zrow[NT];
+  const uint32_t* ctile = a.qw.codes + static_cast<int64_t>(n0) * a.qw.wpr;
+  const float* stile = a.qw.scales + static_cast<int64_t>(n0) * a.qw.gpr;
+  const float* ztile = a.qw.zeros + static_cast<int64_t>(n0) * a.qw.gpr;
+  uint32_t coff[NT], soff[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int64_t n = min(n0 + j * 16 + lr, a.N - 1);   // rows past N repeat the last
-    crow[j] = a.qw.codes + n * a.qw.wpr;
-    srow[j] = a.qw.scales + n * a.qw.gpr;
-    zrow[j] = a.qw.zeros + n * a.qw.gpr;
+    const int n = min(j * 16 + lr, a.N - 1 - n0);       // rows past N repeat the last
+    coff[j] = 4u * n * a.qw.wpr;
+    soff[j] = 4u * n * a.qw.gpr;
   }
+  uint32_t xoff[MT][XO];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    Incoming<S, T>::offsets(xoff[i], a.K, t0 + i * Rows<T>::TOK, a.tokens, lane);
   bf16x8 ones;
   {
     const uint32_t o[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     __builtin_memcpy(&ones, o, 16);
   }
+  const uint32_t mask = in_vgpr(Code::MASK);
   const f32x4 zero4 = f32x4{0.f, 0.f, 0.f, 0.f};
   f32x4 acc[MT][NT];
 #pragma unroll
@@ -387,9 +475,12 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
     for (int j = 0; j < NT; ++j) acc[i][j] = zero4;
 
   uint2 en[4];
-  bool first = true;
-  for (int c0 = w; c0 < nchunks || first; c0 += kDecodeWaves * U) {
-    Codes<BITS, S> cw[U][NT];
+  int rp[RPW + 1];
+  int first = 1;
+  int c0 = w;
+#pragma unroll 1
+  do {
+    Code cw[U][NT];
     Incoming<S, T> xr[U][MT];
     float sc[U][NT], zo[U][NT];
 #pragma unroll
@@ -398,21 +489,32 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
       const int g = col >> a.qw.lg_group;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        cw[u][j].load(crow[j], col + 8 * S * lq, a.qw.wpr);
-        sc[u][j] = srow[j][g];
-        zo[u][j] = zrow[j][g];
+        cw[u][j].load(ctile, coff[j], col, 8 * S * lq, a.qw.wpr);
+        sc[u][j] = ld_at<float>(stile + g, soff[j]);
+        zo[u][j] = ld_at<float>(ztile + g, soff[j]);
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        xr[u][i].load(x, a.K, t0 + i * Rows<T>::TOK, a.tokens, col, lane);
+      for (int i = 0; i < MT; ++i) xr[u][i].load(x + col, xoff[i]);
     }
+    asm volatile("" : "+s"(first));     // no peeled copy of the loop for the first turn
     if (first) {
+      first = 0;
+      if (adapter) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t k = static_cast<int64_t>(k0) + i * kThreads + threadIdx.x;
-        if (k < kend) en[i] = uint2{static_cast<uint32_t>(a.E[2 * k + 1]), __float_as_uint(a.c[k])};
+        for (int i = 0; i < 4; ++i) {
+          const int k = min(i * kThreads + static_cast<int>(threadIdx.x), kend - k0 - 1);
+          if (k >= 0) {
+            const int64_t at = static_cast<int64_t>(k0) + k;
+            en[i] = uint2{static_cast<uint32_t>(a.E[2 * at + 1]), __float_as_uint(a.c[at])};
+          }
+        }
+#pragma unroll
+        for (int i = 0; i <= RPW; ++i) rp[i] = a.row_ptr[min(n0 + w * RPW + i, a.N)];
+        if constexpr (LOCAL) {
+          const int zld = zpad(a.K);
+          local_transform(x, a.tokens, a.K, a.log_b, zld, zl);
+        }
       }
-      first = false;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -432,7 +534,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
         }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const bf16x8 wf = cw[u][j].operand(s);
+          const bf16x8 wf = cw[u][j].operand(s, mask);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
             g[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf, s ? g[i][j] : zero4, 0, 0, 0);
@@ -441,7 +543,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const float z = Codes<BITS, S>::OFF + zo[u][j];
+        const float z = Code::OFF + zo[u][j];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -449,7 +551,8 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
             acc[i][j][r] = fmaf(sc[u][j], fmaf(-z, xs[i][r], g[i][j][r]), acc[i][j][r]);
       }
     }
-  }
+    c0 += kDecodeWaves * U;
+  } while (c0 < nchunks);
   float* red = reinterpret_cast<float*>(own[w]);
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -464,31 +567,39 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
     }
 
   // the nonzeros, a wave RPW rows: lpn lanes hold 4 tokens each of one
-  // nonzero's column
-  if (a.zt != nullptr) {
-    const int lpn = min(a.tp, TB) / 4, npw = 64 / lpn;
+  // nonzero's column (LOCAL: one lane, its tokens one after the other)
+  if (adapter) {
+    const int lpn = LOCAL ? 1 : min(a.tp, TB) / 4, npw = 64 / lpn;
     const int sub = lane / lpn;
-    const float* zl = a.zt + t0 + (lane % lpn) * 4;
+    const float* zg = a.zt + t0 + (lane % lpn) * 4;
+    const int zld = zpad(a.K);
     f32x4 s4[RPW];
 #pragma unroll
     for (int i = 0; i < RPW; ++i) s4[i] = zero4;
-    for (int kb = k0;;) {
+    int kb = k0;
+#pragma unroll 1
+    for (;;) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i * kThreads + static_cast<int>(threadIdx.x) < kend - kb)
-          ent[i * kThreads + threadIdx.x] = en[i];
+      for (int i = 0; i < 4; ++i) ent[i * kThreads + threadIdx.x] = en[i];
       __syncthreads();
       const int held = min(kend - kb, kEntries);
 #pragma unroll
       for (int i = 0; i < RPW; ++i) {
         const int e1 = min(rp[i + 1] - kb, held);
-#pragma unroll 4
+#pragma unroll 2
         for (int k = max(rp[i] - kb, 0) + sub; k < e1; k += npw) {
           const uint2 e = ent[k];
-          const f32x4 zv = *reinterpret_cast<const f32x4*>(zl + static_cast<int64_t>(e.x) * a.tp);
           const float cv = __uint_as_float(e.y);
+          if constexpr (LOCAL) {
+            const float* zr = zl + zpad(e.x);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) s4[i][r] = fmaf(cv, zv[r], s4[i][r]);
+            for (int r = 0; r < kLocalTokens; ++r)
+              if (r < a.tokens) s4[i][r] = fmaf(cv, zr[r * zld], s4[i][r]);
+          } else {
+            const f32x4 zv = *reinterpret_cast<const f32x4*>(zg + static_cast<int64_t>(e.x) * a.tp);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s4[i][r] = fmaf(cv, zv[r], s4[i][r]);
+          }
         }
       }
       if (held == kend - kb) break;
@@ -496,10 +607,12 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t k = static_cast<int64_t>(kb) + i * kThreads + threadIdx.x;
-        if (k < kend) en[i] = uint2{static_cast<uint32_t>(a.E[2 * k + 1]), __float_as_uint(a.c[k])};
+        const int64_t at =
+            static_cast<int64_t>(kb) + min(i * kThreads + static_cast<int>(threadIdx.x), kend - kb - 1);
+        en[i] = uint2{static_cast<uint32_t>(a.E[2 * at + 1]), __float_as_uint(a.c[at])};
       }
     }
+#pragma unroll 1
     for (int o = lpn; o < 64; o <<= 1)
 #pragma unroll
       for (int i = 0; i < RPW; ++i)
@@ -512,34 +625,41 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
         for (int r = 0; r < 4; ++r) ad[w * RPW + i][lane * 4 + r] = s4[i][r];
   }
   __syncthreads();
+#pragma unroll 1
   for (int e = threadIdx.x; e < TB * 16 * NT; e += kThreads) {
     const int t = e / (16 * NT), n = e % (16 * NT);
     if (t0 + t >= a.tokens || n0 + n >= a.N) continue;
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) v += __uint_as_float(own[i][t * LD + n]);
-    if (a.zt != nullptr) v = fmaf(a.alpha, ad[n][t], v);
+    if (adapter) v = fmaf(a.alpha, ad[n][t], v);
     Elem<T>::st(y, static_cast<int64_t>(t0 + t) * a.N + n0 + n, v);
   }
 }
 
-template <int BITS, int S, int MT, int NT, typename T>
+template <int BITS, int S, int MT, int NT, typename T, bool LOCAL>
 hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   constexpr int TB = Rows<T>::TOK * MT;
   const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.tokens + TB - 1) / TB);
-  hipLaunchKernelGGL((decode_kernel<BITS, S, MT, NT, T>), grid, dim3(kDecodeWaves * 64), 0, s, x, a,
+  const size_t lds = LOCAL ? static_cast<size_t>(a.tokens) * (a.K + a.K / 16) * 4 : 0;
+  hipLaunchKernelGGL((decode_kernel<BITS, S, MT, NT, T, LOCAL>), grid, dim3(kThreads), lds, s, x, a,
                      y);
   return hipGetLastError();
 }
 
+// tokens few enough for the transform in LDS
+bool is_local(int T, int K) { return T <= kLocalTokens && T * K <= kLocal; }
+
 template <int BITS, int S, typename T>
 hipError_t decode_s(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
+  if (a.row_ptr != nullptr && is_local(a.tokens, a.K))
+    return decode_t<BITS, S, 1, 1, T, true>(x, a, y, s);
   const int tiles = (a.tokens + Rows<T>::TOK - 1) / Rows<T>::TOK;
   if (tiles == 1)
-    return a.N >= 8192 ? decode_t<BITS, S, 1, 2, T>(x, a, y, s)
-                       : decode_t<BITS, S, 1, 1, T>(x, a, y, s);
-  if (tiles == 2) return decode_t<BITS, S, 2, 1, T>(x, a, y, s);
-  return decode_t<BITS, S, 4, 1, T>(x, a, y, s);
+    return a.N >= 8192 ? decode_t<BITS, S, 1, 2, T, false>(x, a, y, s)
+                       : decode_t<BITS, S, 1, 1, T, false>(x, a, y, s);
+  if (tiles == 2) return decode_t<BITS, S, 2, 1, T, false>(x, a, y, s);
+  return decode_t<BITS, S, 4, 1, T, false>(x, a, y, s);
 }
 
 template <int BITS, typename T>
@@ -593,7 +713,8 @@ int padded_tokens(int T) {
 }  // namespace
 
 size_t decode_scratch_bytes(int64_t T, int K, int64_t p) {
-  return p > 0 ? static_cast<size_t>(K) * padded_tokens(static_cast<int>(T)) * 4 : 0;
+  if (p == 0 || is_local(static_cast<int>(T), K)) return 0;
+  return static_cast<size_t>(K) * padded_tokens(static_cast<int>(T)) * 4;
 }
 
 hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N,
@@ -605,13 +726,19 @@ hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N
   a.N = N;
   a.tp = padded_tokens(T);
   a.qw = qw;
-  a.zt = p > 0 ? static_cast<float*>(scratch) : nullptr;
-  a.row_ptr = row_ptr;
+  a.zt = nullptr;
+  a.row_ptr = p > 0 ? row_ptr : nullptr;
   a.E = E;
   a.c = c;
   a.alpha = alpha;
+  a.log_b = log_n;
+  const bool through_memory = p > 0 && !is_local(T, a.K);
+  if (through_memory)
+    a.zt = static_cast<float*>(scratch);
+  else
+    a.alpha = alpha / static_cast<float>(1 << log_n);
   auto go = [&](auto* xx, auto* yy) {
-    if (a.zt != nullptr) {
+    if (through_memory) {
       const hipError_t e = fwht_d(xx, T, log_n, nblk, a.tp, static_cast<float*>(scratch), s);
       if (e != hipSuccess) return e;
     }

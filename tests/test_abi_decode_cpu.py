@@ -23,14 +23,14 @@ def q():
 
 def test_layer_decode_validation(q):
     def call(**kw):
-        a = dict(x=FAKE, act=1, T=4, d_in=256, d_out=64, codes=FAKE, s=FAKE, z=FAKE, bits=4,
+        a = dict(x=FAKE, act=1, T=20, d_in=256, d_out=64, codes=FAKE, s=FAKE, z=FAKE, bits=4,
                  group=128, p=500, row_ptr=FAKE, E=FAKE, c=FAKE, alpha=1.0, y=FAKE, ws=FAKE,
                  wsb=0)
         a.update(kw)
         return q.qwha_layer_decode(a["x"], a["act"], a["T"], a["d_in"], a["d_out"], a["codes"],
                                    a["s"], a["z"], a["bits"], a["group"], a["p"], a["row_ptr"],
                                    a["E"], a["c"], a["alpha"], a["y"], a["ws"], a["wsb"], None)
-    need = q.qwha_layer_decode_workspace_bytes(4, 256, 64, 500)
+    need = q.qwha_layer_decode_workspace_bytes(20, 256, 64, 500)
     assert need > 0
     assert call() == WORKSPACE
     assert call(wsb=need - 1) == WORKSPACE

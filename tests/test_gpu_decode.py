@@ -239,7 +239,8 @@ def test_two_streams_at_once(q):
 
 
 def test_workspace_refusal(q):
+    # 20 tokens: their transforms go through memory
     L = layer(64, 256, 4, 64, 500, seed=1)
-    x = to_dev(tokens(2, 256, "bf16", 2))
+    x = to_dev(tokens(20, 256, "bf16", 2))
     with pytest.raises(q.QwhaError, match="workspace"):
         q.qwha_layer_decode(x, *weights(L), *adapter(L), ws=q.workspace(16, DEV))
