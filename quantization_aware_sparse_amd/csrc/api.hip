@@ -594,7 +594,7 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
 
 size_t qwha_layer_decode_workspace_bytes(int64_t T, int32_t d_in, int32_t d_out, int64_t p) {
   if (T < 0 || T > QWHA_DECODE_MAX_T || d_in < 1 || d_out < 1 || p < 0) return 0;
-  return align256(decode_scratch_bytes(T, d_in, p));
+  return align256(decode_scratch_bytes(static_cast<int>(T), d_in, d_out, p));
 }
 
 qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t d_in,

@@ -15,28 +15,6 @@ namespace qwha {
 namespace {
 
 // Lanes of a row hold 16 consecutive columns each; N / 16 lanes a row.
-// Partner lanes of the butterflies, through DPP within rows of 16 lanes:
-// lane ^ 1 and ^ 2 are quad permutes, ^ 4 is the mirror of half a row
-// (lane ^ 7) after the reversal of each quad (lane ^ 3), ^ 8 a rotation by 8.
-template <int X>
-__device__ __forceinline__ int lane_xor_i32(int v) {
-  if constexpr (X == 1) return dpp_i32<0xB1>(v);
-  else if constexpr (X == 2) return dpp_i32<0x4E>(v);
-  else if constexpr (X == 4) return dpp_i32<0x141>(dpp_i32<0x1B>(v));
-  else return dpp_i32<0x128>(v);
-}
-template <int X>
-__device__ __forceinline__ float lane_xor(float v) {
-  return __int_as_float(lane_xor_i32<X>(__float_as_int(v)));
-}
-template <int X>
-__device__ __forceinline__ double lane_xor(double v) {
-  const long long b = __double_as_longlong(v);
-  const int lo = lane_xor_i32<X>(static_cast<int>(b));
-  const int hi = lane_xor_i32<X>(static_cast<int>(b >> 32));
-  return __longlong_as_double((static_cast<long long>(hi) << 32) | static_cast<unsigned int>(lo));
-}
-
 template <int X, typename Acc>
 __device__ __forceinline__ void butterfly_lanes(Acc* v, int lane) {
   const bool upper = (lane & X) != 0;

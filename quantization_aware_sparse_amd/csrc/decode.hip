@@ -2,10 +2,15 @@
 // papernotes.org, 损失函数 / 训练策略; gist.science summary §4):
 //   y = x W_Q^T + alpha z F^T,  z = FWHT(x) / b,  T <= 64 tokens.
 //
-//   decode_fwht_kernel  z, transposed: zt[column][token], so that one nonzero
-//                       of F finds its column's tokens side by side;
-//   decode_kernel       the base product on the bf16 matrix cores, the codes
-//                       read once, and the nonzeros of the same rows of F.
+//   decode_kernel       up to 16 bf16 or 4 fp32 tokens: the base product on the
+//                       bf16 matrix cores, the codes read once, K split over
+//                       the waves of a workgroup, and the nonzeros of the same
+//                       rows of F;
+//   decode_wide_kernel  more tokens: K split over workgroups, partial sums;
+//   decode_finish_kernel  the partial sums and the nonzeros of F added up;
+//   decode_z_kernel     z, transposed: zt[column][token], so that one nonzero
+//                       of F finds its column's tokens side by side (left out
+//                       where decode_kernel transforms the tokens itself).
 //
 // The base product per group g of columns, with codes q and OFF = 2^bits:
 //   sum_j x_j (q_j - z) s = s (sum_j x_j (OFF + q_j) - (OFF + z) sum_j x_j).
@@ -27,15 +32,17 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kDecodeWaves = 8;
+constexpr int kThreads = kDecodeWaves * 64;
+constexpr int kSpan = 128;      // columns of a span: 32 per quarter of the wave
 
-// (x & mask) | bits in one instruction: the mask in a vector register (one
-// scalar operand per instruction), the bits a scalar
+// (x & mask) | bits in one instruction, where the mask is in a vector register
+// (one scalar operand per instruction). Left to the compiler: it knows the wait
+// states between the instruction's result and a matrix instruction that reads it.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  uint32_t d;
-  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d) : "v"(x), "v"(mask), "s"(bits));
-  return d;
+  return (x & mask) | bits;
 }
 __device__ __forceinline__ uint32_t in_vgpr(uint32_t v) {
   asm volatile("" : "+v"(v));
@@ -49,168 +56,167 @@ __device__ __forceinline__ V ld_at(const void* base, uint32_t off) {
   return *reinterpret_cast<const V*>(static_cast<const char*>(base) + off);
 }
 
-// ---- a lane's codes of a chunk: 8 S consecutive columns of one row, as S
-// operands of 8 columns each (bf16 of OFF + q, two to a word). `base` is the
-// first row of the tile, `off` the lane's row in bytes, `col` the lane's first
-// column (chunk plus `part`); MASK selects a code in both halves of a word.
-template <int BITS, int S>
-struct Codes;
+__device__ __forceinline__ bf16x8 as_operand(const uint32_t* d) {
+  bf16x8 r;
+  __builtin_memcpy(&r, d, 16);
+  return r;
+}
 
-template <int S>
-struct Codes<4, S> {
-  static constexpr float OFF = 16.f;
-  static constexpr uint32_t MASK = 0x00780078u;
-  uint32_t w[S];
-  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
-                                       int) {
-    const uint32_t* b = base + chunk / 8;
-    const uint32_t o = off + part / 2;
-    if constexpr (S == 4) {
-      const uint4 v = ld_at<uint4>(b, o);
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else if constexpr (S == 2) {
-      const uint2 v = ld_at<uint2>(b, o);
-      w[0] = v.x; w[1] = v.y;
-    } else {
-      w[0] = ld_at<uint32_t>(b, o);
-    }
-  }
-  // bf16(16 + q) = 0x4180 | q << 3: low nibbles from w << 3, high ones from
-  // w >> 1, a byte of each to a pair
-  __device__ __forceinline__ bf16x8 operand(int i, uint32_t mask) const {
-    const uint32_t u = w[i] << 3, v = w[i] >> 1;
-    uint32_t d[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      d[k] = and_or(__builtin_amdgcn_perm(v, u, 0x0C040C00u + 0x00010001u * k), mask, 0x41804180u);
-    bf16x8 r;
-    __builtin_memcpy(&r, d, 16);
-    return r;
-  }
-};
+// ---- codes
+// Lane l reads row l % 16 and, in quarter l / 16 of the wave, the 32 columns
+// 32 (l / 16) .. of a span: 64 consecutive bytes of a row of 4-bit codes. They
+// are four units of 8 columns, one per matrix instruction. The columns that
+// one instruction adds up must share a group. Groups of 128 and more do; for
+// smaller ones the units change places between quarters (an exchange of index
+// bits, unit (a1 a0) of quarter (b1 b0)):
+//   group 64:  a1 <-> b1: units 0 and 1 then hold the span's first group;
+//   group 32:  and a0 <-> b0: unit i holds group i.
+// unit_piece() is the piece of 8 columns that a unit then holds.
+enum Mode { kWide = 0, kHalf = 1, kFull = 2 };    // group >= 128, 64, 32
 
-template <int S>
-struct Codes<2, S> {
-  static constexpr float OFF = 4.f;
-  static constexpr uint32_t MASK = 0x00600060u;
-  uint32_t w[S == 4 ? 2 : 1];
-  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
-                                       int) {
-    const uint32_t* b = base + chunk / 16;
-    const uint32_t o = off + part / 4;
-    if constexpr (S == 4) {
-      const uint2 v = ld_at<uint2>(b, o);
-      w[0] = v.x; w[1] = v.y;
-    } else if constexpr (S == 2) {
-      w[0] = ld_at<uint32_t>(b, o);
-    } else {
-      w[0] = ld_at<uint16_t>(b, o);
-    }
-  }
-  // bf16(4 + q) = 0x4080 | q << 5
-  __device__ __forceinline__ bf16x8 operand(int i, uint32_t mask) const {
-    const uint32_t x = w[i / 2] >> (16 * (i % 2));
-    uint32_t d[4];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      d[2 * k] = and_or(__builtin_amdgcn_perm(x << 3, x << 5, 0x0C040C00u + 0x00010001u * k),
-                        mask, 0x40804080u);
-      d[2 * k + 1] = and_or(__builtin_amdgcn_perm(x >> 1, x << 1, 0x0C040C00u + 0x00010001u * k),
-                            mask, 0x40804080u);
-    }
-    bf16x8 r;
-    __builtin_memcpy(&r, d, 16);
-    return r;
-  }
-};
+template <int MODE>
+__device__ __forceinline__ int unit_piece(int s, int q) {
+  if (MODE == kWide) return 4 * q + s;
+  if (MODE == kHalf) return 4 * (2 * (s >> 1) + (q & 1)) + 2 * (q >> 1) + (s & 1);
+  return 4 * s + q;
+}
 
-// 3-bit codes, 10 to a word: the words' 30-bit contents joined to one string
-// of bits, shifted so that the lane's first code is at bit 0
-template <int S>
-struct Codes<3, S> {
-  static constexpr float OFF = 8.f;
-  static constexpr int NW = S == 4 ? 5 : S == 2 ? 3 : 2;   // (9 + 8 S) / 10 words, rounded up
-  static constexpr int NL = S == 4 ? 3 : S == 2 ? 2 : 1;   // 24 S bits
-  static constexpr uint32_t MASK = 0x00700070u;
+// a's upper 32 lanes <-> b's lower ones; a's odd rows of 16 lanes <-> b's even
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+template <int BITS>
+struct Codes {
+  static constexpr float OFF = BITS == 8 ? 0.f : static_cast<float>(1 << BITS);
+  // a code in both halves of a word, where bf16(OFF + q) has it; OFF's bits
+  static constexpr uint32_t MASK = BITS == 2 ? 0x00600060u : BITS == 3 ? 0x00700070u : 0x00780078u;
+  static constexpr uint32_t BASE = BITS == 2 ? 0x40804080u : BITS == 3 ? 0x41004100u : 0x41804180u;
+  static constexpr int UW = BITS == 8 ? 2 : 1;        // words per unit
+  static constexpr int NW = BITS == 2 ? 2 : BITS == 8 ? 8 : 4;   // words read
+
   uint32_t w[NW];
-  int sh;
-  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
-                                       int wpr) {
-    const int col = chunk + part, word = col / 10;
-    sh = 3 * (col - 10 * word);
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = ld_at<uint32_t>(base, off + 4 * min(word + i, wpr - 1));
-  }
-  __device__ __forceinline__ uint32_t limb(int i) const {
-    const uint32_t lo = (i < NW ? w[i] & 0x3FFFFFFFu : 0u) >> (2 * i);
-    return lo | (i + 1 < NW ? w[i + 1] << (30 - 2 * i) : 0u);
-  }
-  // bf16(8 + q) = 0x4100 | q << 4
-  __device__ __forceinline__ bf16x8 operand(int i, uint32_t mask) const {
-    uint32_t m[NL + 1];
-#pragma unroll
-    for (int k = 0; k < NL; ++k) m[k] = __builtin_amdgcn_alignbit(limb(k + 1), limb(k), sh);
-    m[NL] = 0u;
-    uint32_t d[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int bit = 24 * i + 6 * k;
-      const uint32_t t =
-          __builtin_amdgcn_alignbit(m[bit / 32 + 1 < NL ? bit / 32 + 1 : NL], m[bit / 32], bit % 32) &
-          63u;
-      d[k] = and_or((t << 4) | (t << 17), mask, 0x41004100u);
-    }
-    bf16x8 r;
-    __builtin_memcpy(&r, d, 16);
-    return r;
-  }
-};
+  int sh;     // 3-bit codes
 
-template <int S>
-struct Codes<8, S> {
-  static constexpr float OFF = 0.f;
-  static constexpr uint32_t MASK = 0u;
-  uint32_t w[2 * S];
-  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int chunk, int part,
-                                       int) {
-    const uint32_t* b = base + chunk / 4;
-    const uint32_t o = off + part;
-    if constexpr (S == 1) {
-      const uint2 v = ld_at<uint2>(b, o);
+  // `base`: the tile's first row; `off`: the lane's row, in bytes; `col`: the
+  // lane's first column, 32 columns inside the row
+  __device__ __forceinline__ void load(const uint32_t* base, uint32_t off, int col) {
+    if constexpr (BITS == 2) {
+      const uint2 v = ld_at<uint2>(base, off + col / 4);
       w[0] = v.x; w[1] = v.y;
-    } else {
+    } else if constexpr (BITS == 4) {
+      const uint4 v = ld_at<uint4>(base, off + col / 2);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (BITS == 8) {
 #pragma unroll
-      for (int i = 0; i < S / 2; ++i) {
-        const uint4 v = ld_at<uint4>(b, o + 16 * i);
+      for (int i = 0; i < 2; ++i) {
+        const uint4 v = ld_at<uint4>(base, off + col + 16 * i);
         w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+    } else {
+      // 10 codes to a word: col is a multiple of 32, so the 32 codes start at
+      // an even one and lie in 4 words; the row has them, since for col = K - 32
+      // floor((K - 32) / 10) + 4 = floor((K + 8) / 10) <= ceil(K / 10)
+      const int word = col / 10;
+      sh = 3 * (col - 10 * word);
+      const u32x4_any v = ld_at<u32x4_any>(base, off + 4 * word);
+      w[0] = v[0]; w[1] = v[1]; w[2] = v[2]; w[3] = v[3];
+    }
+  }
+
+  // the four units, in place of the words
+  template <int MODE>
+  __device__ __forceinline__ void units(uint32_t (&u)[4][UW]) const {
+    if constexpr (BITS == 2) {
+      u[0][0] = w[0]; u[1][0] = w[0] >> 16; u[2][0] = w[1]; u[3][0] = w[1] >> 16;
+    } else if constexpr (BITS == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i][0] = w[i];
+    } else if constexpr (BITS == 8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { u[i][0] = w[2 * i]; u[i][1] = w[2 * i + 1]; }
+    } else {
+      // the words' 30-bit contents as one string of bits, from bit sh on
+      const uint32_t l0 = (w[0] & 0x3FFFFFFFu) | (w[1] << 30);
+      const uint32_t l1 = ((w[1] & 0x3FFFFFFFu) >> 2) | (w[2] << 28);
+      const uint32_t l2 = ((w[2] & 0x3FFFFFFFu) >> 4) | (w[3] << 26);
+      const uint32_t l3 = (w[3] & 0x3FFFFFFFu) >> 6;
+      const uint32_t m0 = __builtin_amdgcn_alignbit(l1, l0, sh);
+      const uint32_t m1 = __builtin_amdgcn_alignbit(l2, l1, sh);
+      const uint32_t m2 = __builtin_amdgcn_alignbit(l3, l2, sh);
+      u[0][0] = m0;                                        // 24 bits each
+      u[1][0] = __builtin_amdgcn_alignbit(m1, m0, 24);
+      u[2][0] = __builtin_amdgcn_alignbit(m2, m1, 16);
+      u[3][0] = m2 >> 8;
+    }
+    if constexpr (MODE != kWide) {
+#pragma unroll
+      for (int i = 0; i < UW; ++i) {
+        swap32(u[0][i], u[2][i]);
+        swap32(u[1][i], u[3][i]);
+        if constexpr (MODE == kFull) {
+          swap16(u[0][i], u[1][i]);
+          swap16(u[2][i], u[3][i]);
+        }
       }
     }
   }
-  // the upper halves of fp32(q): exact, q < 2^8
-  __device__ __forceinline__ bf16x8 operand(int i, uint32_t) const {
+
+  // 8 codes as bf16(OFF + q), two to a word
+  static __device__ __forceinline__ bf16x8 operand(const uint32_t (&u)[UW], uint32_t mask) {
     uint32_t d[4];
+    if constexpr (BITS == 8) {
+      // the upper halves of fp32(q): exact, q < 2^8
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t x = w[2 * i + k / 2] >> (16 * (k % 2));
-      const uint32_t a = __float_as_uint(static_cast<float>(x & 0xFFu));
-      const uint32_t b = __float_as_uint(static_cast<float>((x >> 8) & 0xFFu));
-      d[k] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t x = u[k / 2] >> (16 * (k % 2));
+        const uint32_t lo = __float_as_uint(static_cast<float>(x & 0xFFu));
+        const uint32_t hi = __float_as_uint(static_cast<float>((x >> 8) & 0xFFu));
+        d[k] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+      }
+    } else if constexpr (BITS == 4) {
+      // low nibbles from u << 3, high ones from u >> 1, a byte of each to a pair
+      const uint32_t lo = u[0] << 3, hi = u[0] >> 1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        d[k] = and_or(__builtin_amdgcn_perm(hi, lo, 0x0C040C00u + 0x00010001u * k), mask, BASE);
+    } else if constexpr (BITS == 2) {
+      const uint32_t a = u[0] << 5, b = u[0] << 3, c = u[0] << 1, e = u[0] >> 1;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t sel = 0x0C040C00u + 0x00010001u * k;
+        d[2 * k] = and_or(__builtin_amdgcn_perm(b, a, sel), mask, BASE);
+        d[2 * k + 1] = and_or(__builtin_amdgcn_perm(e, c, sel), mask, BASE);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t t = (u[0] >> (6 * k)) & 63u;
+        d[k] = and_or((t << 4) | (t << 17), mask, BASE);
+      }
     }
-    bf16x8 r;
-    __builtin_memcpy(&r, d, 16);
-    return r;
+    return as_operand(d);
   }
 };
 
-// ---- tokens as rows of the matrix instruction, staged by each wave for itself
-// in LDS: 128-byte lines in, operands out. A chunk is 32 S columns of 16 rows;
-// 16-byte piece p of row m lies at piece p ^ (m % pieces) of its row, so that
-// the rows one read covers hit distinct banks.
+// ---- tokens, staged in LDS as rows of the matrix instruction
+// A tile is 16 rows of a span; 16-byte piece p of row m lies at piece
+// p ^ m of its row, so that the rows one read covers hit distinct banks.
+constexpr int kTileWords = 16 * kSpan / 2;
+__device__ __forceinline__ int tile_at(int row, int piece) { return row * 64 + ((piece ^ row) & 15) * 4; }
+
 template <typename T>
 struct Rows;
 template <>
 struct Rows<uint16_t> {
-  static constexpr int TOK = 16;     // tokens per 16 rows
+  static constexpr int TOK = 16;     // tokens per tile
 };
 // fp32 tokens: rows 4i .. 4i + 2 are a token's upper, middle and lower 8 bits
 // of mantissa (each what is left of x after the one before, cut to bf16:
@@ -220,57 +226,27 @@ struct Rows<float> {
   static constexpr int TOK = 4;
 };
 
-template <int S>
-struct Stage {
-  static constexpr int PIECES = 4 * S;                 // of 16 bytes, per row
-  static constexpr int WORDS = 16 * 16 * S;            // of 4 bytes, per 16 rows
-  static __device__ __forceinline__ int at(int row, int piece) {
-    return (row * PIECES + (piece ^ (row % PIECES))) * 4;
+// 8 columns of one token, between memory and LDS.
+template <typename T>
+struct Piece;
+template <>
+struct Piece<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* x, uint32_t row_off, int col) {
+    v = ld_at<uint4>(x, row_off + 2 * col);
+  }
+  __device__ __forceinline__ void store(uint32_t* tile, int tok, int piece) const {
+    *reinterpret_cast<uint4*>(tile + tile_at(tok, piece)) = v;
   }
 };
-
-// A wave's part of a chunk on its way from memory to LDS. Rows past the last
-// token repeat it (their results are not stored).
-template <int S, typename T>
-struct Incoming;
-template <int S>
-struct Incoming<S, uint16_t> {
-  uint4 v[S];
-  // byte offsets of a lane's pieces in x
-  static __device__ __forceinline__ void offsets(uint32_t* off, int K, int t0, int tokens,
-                                                 int lane) {
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int e = i * 64 + lane;
-      off[i] = 2 * (min(t0 + e / (4 * S), tokens - 1) * K + 8 * (e % (4 * S)));
-    }
-  }
-  __device__ __forceinline__ void load(const uint16_t* x, const uint32_t* off) {
-#pragma unroll
-    for (int i = 0; i < S; ++i) v[i] = ld_at<uint4>(x, off[i]);
-  }
-  __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int e = i * 64 + lane;
-      *reinterpret_cast<uint4*>(lds + Stage<S>::at(e / (4 * S), e % (4 * S))) = v[i];
-    }
-  }
-};
-template <int S>
-struct Incoming<S, float> {
+template <>
+struct Piece<float> {
   float4 v[2];
-  static __device__ __forceinline__ void offsets(uint32_t* off, int K, int t0, int tokens,
-                                                 int lane) {
-    // lanes past 16 S have no piece of their own
-    off[0] = 4 * (min(t0 + lane / (4 * S), tokens - 1) * K + 8 * (lane % (4 * S)));
+  __device__ __forceinline__ void load(const float* x, uint32_t row_off, int col) {
+    v[0] = ld_at<float4>(x, row_off + 4 * col);
+    v[1] = ld_at<float4>(x, row_off + 4 * col + 16);
   }
-  __device__ __forceinline__ void load(const float* x, const uint32_t* off) {
-    v[0] = ld_at<float4>(x, off[0]);
-    v[1] = ld_at<float4>(x, off[0] + 16);
-  }
-  __device__ __forceinline__ void store(uint32_t* lds, int lane) const {
-    const int tok = lane / (4 * S), piece = lane % (4 * S);
+  __device__ __forceinline__ void store(uint32_t* tile, int tok, int piece) const {
     const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t h[3][8];
 #pragma unroll
@@ -280,393 +256,586 @@ struct Incoming<S, float> {
       h[1][i] = __float_as_uint(r1);
       h[2][i] = __float_as_uint(r1 - __uint_as_float(h[1][i] & 0xFFFF0000u));
     }
-    if (tok < 4) {
 #pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        uint32_t d[4] = {0u, 0u, 0u, 0u};
-        if (part < 3)
+    for (int part = 0; part < 4; ++part) {
+      uint32_t d[4] = {0u, 0u, 0u, 0u};
+      if (part < 3)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            d[i] = __builtin_amdgcn_perm(h[part][2 * i + 1], h[part][2 * i], 0x07060302u);
-        *reinterpret_cast<uint4*>(lds + Stage<S>::at(4 * tok + part, piece)) =
-            uint4{d[0], d[1], d[2], d[3]};
-      }
+        for (int i = 0; i < 4; ++i)
+          d[i] = __builtin_amdgcn_perm(h[part][2 * i + 1], h[part][2 * i], 0x07060302u);
+      *reinterpret_cast<uint4*>(tile + tile_at(4 * tok + part, piece)) = uint4{d[0], d[1], d[2], d[3]};
     }
   }
 };
 
-// ---- the transform of the tokens, zt[column][tp] fp32: four tokens of a
-// block side by side in a workgroup, so that a column's values leave together
-template <int LOG_N>
-struct Zt {
-  using F = Fwht<LOG_N>;
-  static constexpr int TT = LOG_N <= 12 ? 4 : LOG_N == 13 ? 2 : 1;     // tokens side by side
-  static constexpr int BLOCK = F::TPR * TT > 256 ? F::TPR * TT : 256;
-  static constexpr int BLKS = BLOCK / (F::TPR * TT);                   // blocks of columns
+struct DecodeArgs {
+  int tokens, K, N, tp;
+  QuantW qw;
+  const float* zt;             // zt[column][tp], where z goes through memory
+  const int32_t* row_ptr;      // null without an adapter
+  const int32_t* E;
+  const float* c;
+  float alpha;                 // alpha / b for the plain sums of a transform in LDS
+  int log_b;
+  float* part;                 // decode_wide_kernel: [slices][tokens][N]
+  int slices;
 };
-template <int LOG_N, typename TIn>
-__global__ __launch_bounds__(Zt<LOG_N>::BLOCK) void decode_fwht_kernel(const TIn* __restrict__ x,
-                                                                       int tokens, int nblk,
-                                                                       int tp,
-                                                                       float* __restrict__ zt) {
-  using F = Fwht<LOG_N>;
-  using Z = Zt<LOG_N>;
-  __shared__ float lds_all[Z::BLKS * Z::TT * F::LDS];
-  const int slot = threadIdx.x / F::TPR, u = threadIdx.x % F::TPR;
-  const int blk = blockIdx.x * Z::BLKS + slot / Z::TT, t = blockIdx.y * Z::TT + slot % Z::TT;
-  const int64_t K = static_cast<int64_t>(nblk) << LOG_N;
-  float* lds = lds_all + slot * F::LDS;
-  float v[16];
-  if (blk < nblk && t < tokens) {
-    load16(x + t * K + (static_cast<int64_t>(blk) << LOG_N) + u * 16, v);
-  } else {
+
+// The product of one span: acc += s (x (OFF + q) - (OFF + z) sum x), group by
+// group. Lane l's results: W's row l % 16 of tile j and the token rows
+// 4 (l / 16) .. + 4 of tile i.
+template <int BITS, int MODE, int MT, int NT>
+__device__ __forceinline__ void span_product(const uint32_t* tiles, const Codes<BITS> (&cw)[NT],
+                                             const float (&sc)[NT][1 << MODE],
+                                             const float (&zo)[NT][1 << MODE], bool half_span,
+                                             uint32_t mask, bf16x8 ones, int lr, int lq,
+                                             f32x4 (&acc)[MT][NT]) {
+  using Code = Codes<BITS>;
+  constexpr int G = 1 << MODE, PER = 4 / G;    // groups, instructions per group
+  const f32x4 zero4 = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint32_t u[NT][4][Code::UW];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) v[r] = 0.f;
-  }
-  F::run(v, lds, u);
-  constexpr float scale = 1.f / static_cast<float>(F::N);
-  __syncthreads();
+  for (int j = 0; j < NT; ++j) cw[j].template units<MODE>(u[j]);
+  f32x4 g[MT][NT], xs[MT];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) lds[F::pad(F::out_index(u, r))] = v[r] * scale;
-  __syncthreads();
-  const int b0 = blockIdx.x * Z::BLKS, t0 = blockIdx.y * Z::TT;
-  for (int e = threadIdx.x; e < Z::BLKS * F::N; e += Z::BLOCK) {
-    const int bl = e >> LOG_N, j = e & (F::N - 1);
-    if (b0 + bl >= nblk) break;
-    const float* src = lds_all + bl * Z::TT * F::LDS + F::pad(j);
-    float* dst = zt + ((static_cast<int64_t>(b0 + bl) << LOG_N) + j) * tp + t0;
-    if constexpr (Z::TT == 4) {
-      *reinterpret_cast<float4*>(dst) =
-          float4{src[0], src[F::LDS], src[2 * F::LDS], src[3 * F::LDS]};
-    } else {
+  for (int s = 0; s < 4; ++s) {
+    if (MODE != kWide && s == 2 && half_span) break;     // the columns end after two units
+    bf16x8 xf[MT];
 #pragma unroll
-      for (int i = 0; i < Z::TT; ++i) dst[i] = src[i * F::LDS];
+    for (int i = 0; i < MT; ++i) {
+      xf[i] = *reinterpret_cast<const bf16x8*>(tiles + i * kTileWords +
+                                               tile_at(lr, unit_piece<MODE>(s, lq)));
+      xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], ones, s % PER ? xs[i] : zero4, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const bf16x8 wf = Code::operand(u[j][s], mask);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        g[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf, s % PER ? g[i][j] : zero4, 0, 0, 0);
+    }
+    if (s % PER == PER - 1) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const float z = Code::OFF + zo[j][s / PER];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[i][j][r] = fmaf(sc[j][s / PER], fmaf(-z, xs[i][r], g[i][j][r]), acc[i][j][r]);
+      }
     }
   }
 }
 
-// ---- the product
-// A workgroup takes 16 NT rows of W and MT tiles of tokens; its waves take the
-// chunks of 32 S columns in turn, U of them with all loads in flight at once,
-// and add up their sums in LDS. Lane l holds row l % 16 of its tile of W and,
-// of the tokens, row l % 16; both hold the columns 8 S (l / 16) .. + 8 S of the
-// chunk, so a lane reads consecutive bytes of a row of codes and a chunk never
-// crosses a group (32 S <= group). Results: lane l has W's row l % 16 and the
-// token rows 4 (l / 16) .. + 4.
-// The nonzeros of the same rows of F lie side by side in E and c: the first
-// kEntries of them are fetched beside the codes and wait in LDS, so that only
-// the gather of z is left behind the product.
-// With few tokens every workgroup transforms them itself, in LDS, while its
-// codes are on their way (LOCAL): one launch, and no way through memory for z.
-// The code is kept short (loops, no peeled copies): a workgroup runs through
-// most of it once, and fetching instructions costs as much as fetching codes.
-struct DecodeArgs {
-  int tokens, K, N, tp;
-  QuantW qw;
-  const float* zt;             // zt[column][tp], unless LOCAL or p = 0
-  const int32_t* row_ptr;      // null without an adapter
-  const int32_t* E;
-  const float* c;
-  float alpha;                 // LOCAL: alpha / b, for the plain sums of the transform
-  int log_b;
-};
+__device__ __forceinline__ bf16x8 bf16_ones() {
+  const uint32_t o[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  return as_operand(o);
+}
 
-constexpr int kThreads = kDecodeWaves * 64;
-constexpr int kEntries = 4 * kThreads;   // nonzeros staged at a time
-constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
-constexpr int kLocalTokens = 4;
-
+// ---- the transform in LDS
 __device__ __forceinline__ int zpad(int j) { return j + (j >> 4); }
 
-// z <- x H per block of 2^log_b columns, z[t * zld + zpad(column)], unscaled:
-// passes of 4 index bits, 16 values a thread, in place.
+// 16 consecutive values on their way
 template <typename T>
-__device__ __forceinline__ void local_transform(const T* __restrict__ x, int tokens, int K,
-                                                int log_b, int zld, float* z) {
-  const int per = K >> 4, items = tokens * per;
-  int done = 0;                              // index bits done
+struct Raw16;
+template <>
+struct Raw16<uint16_t> {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    v[0] = reinterpret_cast<const uint4*>(p)[0];
+    v[1] = reinterpret_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+        f[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+    }
+  }
+};
+template <>
+struct Raw16<float> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[4 * i] = v[i].x; f[4 * i + 1] = v[i].y; f[4 * i + 2] = v[i].z; f[4 * i + 3] = v[i].w;
+    }
+  }
+};
+
+__device__ __forceinline__ void butterflies(float* v, int b) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    if (r & (1 << b)) continue;
+    const float p = v[r], q = v[r + (1 << b)];
+    v[r] = p + q;
+    v[r + (1 << b)] = p - q;
+  }
+}
+
+// z[t * zld + zpad(column)] <- x H per block of 2^log_b columns, unscaled:
+// passes of 4 index bits, 16 values a thread, in place. `raw` holds the
+// thread's first 16 values (fetched before anything else is waited for).
+template <typename T>
+__device__ __forceinline__ void local_transform(const T* __restrict__ x, Raw16<T> raw, int items,
+                                                int per, int log_b, int zld, float* z) {
+  float v[16];
 #pragma unroll 1
-  for (int lo = 0; done < log_b; lo = min(lo + 4, log_b - 4)) {
-    const int hi = lo + 4;
+  for (int e = threadIdx.x; e < items;) {
+    raw.get(v);
+    const int t = e / per, u = e - t * per;
+    e += kThreads;
+    if (e < items) raw.load(x + static_cast<int64_t>(e) * 16);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) butterflies(v, b);
+    float* zr = z + t * zld + 17 * u;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) zr[r] = v[r];
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int done = 4; done < log_b; done += 4) {
+    const int lo = min(done, log_b - 4);
 #pragma unroll 1
     for (int e = threadIdx.x; e < items; e += kThreads) {
       const int t = e / per, u = e - t * per;
-      const int j0 = (u & ((1 << lo) - 1)) | ((u >> lo) << hi);
       float* zr = z + t * zld;
-      float v[16];
-      if (done == 0) {
-        load16(x + static_cast<int64_t>(t) * K + u * 16, v);
-      } else {
+      const int j0 = (u & ((1 << lo) - 1)) | ((u >> lo) << (lo + 4));
 #pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] = zr[zpad(j0 + (r << lo))];
-      }
+      for (int r = 0; r < 16; ++r) v[r] = zr[zpad(j0 + (r << lo))];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (lo + b < done) continue;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if (r & (1 << b)) continue;
-          const float p = v[r], q = v[r + (1 << b)];
-          v[r] = p + q;
-          v[r + (1 << b)] = p - q;
-        }
-      }
+      for (int b = 0; b < 4; ++b)
+        if (lo + b >= done) butterflies(v, b);
 #pragma unroll
       for (int r = 0; r < 16; ++r) zr[zpad(j0 + (r << lo))] = v[r];
     }
-    done = hi;
     __syncthreads();
   }
 }
 
-template <int BITS, int S, int MT, int NT, typename T, bool LOCAL>
+// zt[column][tp] of one token per workgroup
+template <typename T>
+__global__ __launch_bounds__(kThreads) void decode_z_kernel(const T* __restrict__ x, int K,
+                                                            int log_b, int tp,
+                                                            float* __restrict__ zt) {
+  extern __shared__ float zl[];
+  const T* row = x + static_cast<int64_t>(blockIdx.x) * K;
+  const int items = K >> 4;
+  Raw16<T> raw;
+  raw.load(row + 16 * min(static_cast<int>(threadIdx.x), items - 1));
+  local_transform(row, raw, items, items, log_b, zpad(K), zl);
+  const float scale = 1.f / static_cast<float>(1 << log_b);
+  for (int j = threadIdx.x; j < K; j += kThreads)
+    zt[static_cast<int64_t>(j) * tp + blockIdx.x] = zl[zpad(j)] * scale;
+}
+
+// ---- the nonzeros of 16 NT rows of F: side by side in E and c. The first
+// kEntries of them are fetched beside the codes and wait in LDS, so that only
+// the gather of z is left behind the product. 64 / RPW lanes take a row.
+constexpr int kEntries = 4 * kThreads;
+constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
+constexpr int kLocalTokens = 4;
+
+struct Entries {
+  uint2 e[4];                            // column, value
+  __device__ __forceinline__ void load(const DecodeArgs& a, int kb, int kend) {
+    if (kend == kb) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at =
+          static_cast<int64_t>(kb) + min(i * kThreads + static_cast<int>(threadIdx.x), kend - kb - 1);
+      e[i] = uint2{static_cast<uint32_t>(a.E[2 * at + 1]), __float_as_uint(a.c[at])};
+    }
+  }
+  __device__ __forceinline__ void store(uint2* ent) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ent[i * kThreads + threadIdx.x] = e[i];
+  }
+};
+
+// Sums over the lanes that differ in the bits from `from` to 64 / RPW (a
+// power of two each): within rows of 16 lanes through DPP.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v, int from) {
+  if (from <= 1) v += lane_xor<1>(v);
+  if (from <= 2) v += lane_xor<2>(v);
+  if (from <= 4) v += lane_xor<4>(v);
+  if (from <= 8) v += lane_xor<8>(v);
+  if constexpr (LANES > 16) {
+    if (from <= 16) v += __shfl_xor(v, 16);
+  }
+  return v;
+}
+
+// ad[row][token] for the workgroup's 8 RPW rows and its tokens t0 ..; entries
+// beyond the staged ones follow in further rounds. LOCAL: z in LDS, a lane a
+// nonzero, its tokens one after the other; else min(tp, TB) / 4 lanes hold 4
+// tokens each of a nonzero's column. All threads call it.
+template <int RPW, bool LOCAL, int LDA>
+__device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2* ent, int k0,
+                                         int kend, int beg, int end, int t0, int lpn,
+                                         const float* zl, float (*ad)[LDA]) {
+  constexpr int LPR = 64 / RPW;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int in_row = lane & (LPR - 1);
+  const int npw = LPR / lpn, sub = in_row / lpn;
+  const float* zg = a.zt + t0 + (in_row & (lpn - 1)) * 4;
+  const int zld = zpad(a.K);
+  f32x4 s4 = f32x4{0.f, 0.f, 0.f, 0.f};
+  int kb = k0;
+#pragma unroll 1
+  for (;;) {
+    en.store(ent);
+    __syncthreads();
+    const int held = min(kend - kb, kEntries);
+    const int e1 = min(end - kb, held);
+#pragma unroll 4
+    for (int k = max(beg - kb, 0) + sub; k < e1; k += npw) {
+      const uint2 e = ent[k];
+      const float cv = __uint_as_float(e.y);
+      if constexpr (LOCAL) {
+        const float* zr = zl + zpad(e.x);
+        s4[0] = fmaf(cv, zr[0], s4[0]);
+        if (a.tokens > 1) {
+#pragma unroll
+          for (int r = 1; r < kLocalTokens; ++r)
+            if (r < a.tokens) s4[r] = fmaf(cv, zr[r * zld], s4[r]);
+        }
+      } else {
+        const f32x4 zv = *reinterpret_cast<const f32x4*>(zg + static_cast<int64_t>(e.x) * a.tp);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s4[r] = fmaf(cv, zv[r], s4[r]);
+      }
+    }
+    if (held == kend - kb) break;
+    kb += held;
+    __syncthreads();
+    en.load(a, kb, kend);
+  }
+  s4[0] = lanes_sum<LPR>(s4[0], lpn);
+  if (a.tokens > 1)
+#pragma unroll
+    for (int r = 1; r < 4; ++r) s4[r] = lanes_sum<LPR>(s4[r], lpn);
+  if (in_row < lpn)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) ad[w * RPW + lane / LPR][in_row * 4 + r] = s4[r];
+}
+
+// ---- up to 16 bf16 or 4 fp32 tokens
+// A workgroup takes 16 NT rows of W; its waves take the spans in turn, D of
+// them on their way at any time, and add up their sums in LDS. With few tokens
+// every workgroup transforms them itself while its codes are on their way
+// (LOCAL): one launch, and no way through memory for z. The code is kept short
+// (loops, no peeled copies): a workgroup runs through much of it once, and
+// fetching instructions costs as much as fetching codes. FEW: at most 4 tokens,
+// of whose tiles only the first 4 rows are staged (the others' results are not
+// used, whatever they hold).
+template <int BITS, int MODE, int NT, typename T, bool FEW, bool LOCAL>
 __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ x, DecodeArgs a,
                                                           T* __restrict__ y) {
-  constexpr int TB = Rows<T>::TOK * MT;              // tokens of the workgroup
-  constexpr int U = 16 / S / MT > 0 ? (16 / S / MT > 4 ? 4 : 16 / S / MT) : 1;
-  constexpr int LD = 16 * NT + 1;
+  constexpr int TB = Rows<T>::TOK;
+  constexpr int D = 4;                               // spans on their way
+  constexpr int G = 1 << MODE;
+  constexpr int PX = sizeof(T) == 2 && !FEW ? 4 : 1; // pieces of a span per lane
   constexpr int RPW = 2 * NT;                        // rows of F per wave
-  constexpr int XW = MT * Stage<S>::WORDS;           // staged words of a wave
-  constexpr int RW = TB * LD;                        // words of a wave's sums
-  // a wave's staged tokens and, later, its sums share their place
-  constexpr int WAVE = ((XW > RW ? XW : RW) + 3) & ~3;
-  constexpr int XO = sizeof(T) == 2 ? S : 1;
-  using Code = Codes<BITS, S>;
-  __shared__ __attribute__((aligned(16))) uint32_t own[kDecodeWaves][WAVE];
-  __shared__ float ad[16 * NT][LOCAL ? 4 : TB + 4];
-  __shared__ uint2 ent[kEntries];                    // column, value
+  constexpr int LD = 16 * NT + 1;
+  using Code = Codes<BITS>;
+  __shared__ __attribute__((aligned(16))) uint32_t own[kDecodeWaves][kTileWords];
+  __shared__ float ad[16 * NT][TB + 4];
+  __shared__ uint2 ent[kEntries];
   extern __shared__ float zl[];                      // LOCAL: [tokens][zpad(K)]
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NT, t0 = blockIdx.y * TB;
-  const int nchunks = a.K / (32 * S);
+  const int n0 = blockIdx.x * 16 * NT;
+  const int spans = (a.K + kSpan - 1) / kSpan;
   const bool adapter = a.row_ptr != nullptr;
 
-  int k0 = 0, kend = 0;
+  int k0 = 0, kend = 0, beg = 0, end = 0;
+  Raw16<T> raw;
   if (adapter) {
     k0 = a.row_ptr[n0];
     kend = a.row_ptr[min(n0 + 16 * NT, a.N)];
+    const int row = n0 + w * RPW + lane / (64 / RPW);
+    beg = a.row_ptr[min(row, a.N)];
+    end = a.row_ptr[min(row + 1, a.N)];
+    if constexpr (LOCAL)
+      raw.load(x + 16 * min(static_cast<int>(threadIdx.x), (a.tokens * a.K >> 4) - 1));
   }
   const uint32_t* ctile = a.qw.codes + static_cast<int64_t>(n0) * a.qw.wpr;
   const float* stile = a.qw.scales + static_cast<int64_t>(n0) * a.qw.gpr;
   const float* ztile = a.qw.zeros + static_cast<int64_t>(n0) * a.qw.gpr;
-  uint32_t coff[NT], soff[NT];
+  uint32_t coff[NT], soff[NT], xoff[PX];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int n = min(j * 16 + lr, a.N - 1 - n0);       // rows past N repeat the last
     coff[j] = 4u * n * a.qw.wpr;
     soff[j] = 4u * n * a.qw.gpr;
   }
-  uint32_t xoff[MT][XO];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    Incoming<S, T>::offsets(xoff[i], a.K, t0 + i * Rows<T>::TOK, a.tokens, lane);
-  bf16x8 ones;
-  {
-    const uint32_t o[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    __builtin_memcpy(&ones, o, 16);
-  }
-  const uint32_t mask = in_vgpr(Code::MASK);
-  const f32x4 zero4 = f32x4{0.f, 0.f, 0.f, 0.f};
-  f32x4 acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = zero4;
+  for (int i = 0; i < PX; ++i)                          // tokens past the last repeat it
+    xoff[i] = sizeof(T) * min(4 * i + lq, a.tokens - 1) * a.K;
 
-  uint2 en[4];
-  int rp[RPW + 1];
-  int first = 1;
-  int c0 = w;
-#pragma unroll 1
-  do {
-    Code cw[U][NT];
-    Incoming<S, T> xr[U][MT];
-    float sc[U][NT], zo[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int col = min(c0 + u * kDecodeWaves, nchunks - 1) * 32 * S;   // in bounds past the end
-      const int g = col >> a.qw.lg_group;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        cw[u][j].load(ctile, coff[j], col, 8 * S * lq, a.qw.wpr);
-        sc[u][j] = ld_at<float>(stile + g, soff[j]);
-        zo[u][j] = ld_at<float>(ztile + g, soff[j]);
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xr[u][i].load(x + col, xoff[i]);
-    }
-    asm volatile("" : "+s"(first));     // no peeled copy of the loop for the first turn
-    if (first) {
-      first = 0;
-      if (adapter) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = min(i * kThreads + static_cast<int>(threadIdx.x), kend - k0 - 1);
-          if (k >= 0) {
-            const int64_t at = static_cast<int64_t>(k0) + k;
-            en[i] = uint2{static_cast<uint32_t>(a.E[2 * at + 1]), __float_as_uint(a.c[at])};
-          }
-        }
-#pragma unroll
-        for (int i = 0; i <= RPW; ++i) rp[i] = a.row_ptr[min(n0 + w * RPW + i, a.N)];
-        if constexpr (LOCAL) {
-          const int zld = zpad(a.K);
-          local_transform(x, a.tokens, a.K, a.log_b, zld, zl);
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c0 + u * kDecodeWaves >= nchunks) break;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xr[u][i].store(&own[w][i * Stage<S>::WORDS], lane);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      f32x4 g[MT][NT], xs[MT];
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        bf16x8 xf[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          xf[i] = *reinterpret_cast<const bf16x8*>(
-              &own[w][i * Stage<S>::WORDS + Stage<S>::at(lr, lq * S + s)]);
-          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], ones, s ? xs[i] : zero4, 0, 0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const bf16x8 wf = cw[u][j].operand(s, mask);
-#pragma unroll
-          for (int i = 0; i < MT; ++i)
-            g[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], wf, s ? g[i][j] : zero4, 0, 0, 0);
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const float z = Code::OFF + zo[u][j];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[i][j][r] = fmaf(sc[u][j], fmaf(-z, xs[i][r], g[i][j][r]), acc[i][j][r]);
-      }
-    }
-    c0 += kDecodeWaves * U;
-  } while (c0 < nchunks);
-  float* red = reinterpret_cast<float*>(own[w]);
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
+  struct Slot {
+    Code cw[NT];
+    float sc[NT][G], zo[NT][G];
+    Piece<T> xp[PX];
+  } slot[D];
+  auto fetch = [&](Slot& s, int span) {
+    const int c0 = min(span, spans - 1) * kSpan;        // in bounds past the end
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      if constexpr (sizeof(T) == 2) {
+      s.cw[j].load(ctile, coff[j], min(c0 + 32 * lq, a.K - 32));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) red[(i * 16 + 4 * lq + r) * LD + j * 16 + lr] = acc[i][j][r];
-      } else {
-        red[(i * 4 + lq) * LD + j * 16 + lr] = acc[i][j][0] + acc[i][j][1] + acc[i][j][2];
+      for (int g = 0; g < G; ++g) {
+        const int gi = MODE == kWide ? c0 >> a.qw.lg_group : min((c0 >> a.qw.lg_group) + g, a.qw.gpr - 1);
+        s.sc[j][g] = ld_at<float>(stile + gi, soff[j]);
+        s.zo[j][g] = ld_at<float>(ztile + gi, soff[j]);
       }
     }
-
-  // the nonzeros, a wave RPW rows: lpn lanes hold 4 tokens each of one
-  // nonzero's column (LOCAL: one lane, its tokens one after the other)
+#pragma unroll
+    for (int i = 0; i < PX; ++i) s.xp[i].load(x, xoff[i], min(c0 + 8 * lr, a.K - 8));
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(slot[d], w + d * kDecodeWaves);
+  Entries en;
   if (adapter) {
-    const int lpn = LOCAL ? 1 : min(a.tp, TB) / 4, npw = 64 / lpn;
-    const int sub = lane / lpn;
-    const float* zg = a.zt + t0 + (lane % lpn) * 4;
-    const int zld = zpad(a.K);
-    f32x4 s4[RPW];
-#pragma unroll
-    for (int i = 0; i < RPW; ++i) s4[i] = zero4;
-    int kb = k0;
-#pragma unroll 1
-    for (;;) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ent[i * kThreads + threadIdx.x] = en[i];
-      __syncthreads();
-      const int held = min(kend - kb, kEntries);
-#pragma unroll
-      for (int i = 0; i < RPW; ++i) {
-        const int e1 = min(rp[i + 1] - kb, held);
-#pragma unroll 2
-        for (int k = max(rp[i] - kb, 0) + sub; k < e1; k += npw) {
-          const uint2 e = ent[k];
-          const float cv = __uint_as_float(e.y);
-          if constexpr (LOCAL) {
-            const float* zr = zl + zpad(e.x);
-#pragma unroll
-            for (int r = 0; r < kLocalTokens; ++r)
-              if (r < a.tokens) s4[i][r] = fmaf(cv, zr[r * zld], s4[i][r]);
-          } else {
-            const f32x4 zv = *reinterpret_cast<const f32x4*>(zg + static_cast<int64_t>(e.x) * a.tp);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s4[i][r] = fmaf(cv, zv[r], s4[i][r]);
-          }
-        }
-      }
-      if (held == kend - kb) break;
-      kb += held;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t at =
-            static_cast<int64_t>(kb) + min(i * kThreads + static_cast<int>(threadIdx.x), kend - kb - 1);
-        en[i] = uint2{static_cast<uint32_t>(a.E[2 * at + 1]), __float_as_uint(a.c[at])};
-      }
-    }
-#pragma unroll 1
-    for (int o = lpn; o < 64; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < RPW; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s4[i][r] += __shfl_xor(s4[i][r], o);
-    if (lane < lpn)
-#pragma unroll
-      for (int i = 0; i < RPW; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) ad[w * RPW + i][lane * 4 + r] = s4[i][r];
+    en.load(a, k0, kend);
+    if constexpr (LOCAL)
+      local_transform(x, raw, a.tokens * a.K >> 4, a.K >> 4, a.log_b, zpad(a.K), zl);
   }
-  __syncthreads();
+
+  const uint32_t mask = in_vgpr(Code::MASK);
+  const bf16x8 ones = bf16_ones();
+  f32x4 acc[1][NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-  for (int e = threadIdx.x; e < TB * 16 * NT; e += kThreads) {
+  for (int s0 = w; s0 < spans; s0 += D * kDecodeWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int span = s0 + d * kDecodeWaves;
+      if (span >= spans) break;
+#pragma unroll
+      for (int i = 0; i < PX; ++i) slot[d].xp[i].store(own[w], 4 * i + lq, lr);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      span_product<BITS, MODE, 1, NT>(own[w], slot[d].cw, slot[d].sc, slot[d].zo,
+                                      a.K - span * kSpan < kSpan, mask, ones, lr, lq, acc);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (span + D * kDecodeWaves < spans) fetch(slot[d], span + D * kDecodeWaves);
+    }
+  }
+  float* red = reinterpret_cast<float*>(own[w]);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) red[(4 * lq + r) * LD + j * 16 + lr] = acc[0][j][r];
+    } else {
+      red[lq * LD + j * 16 + lr] = acc[0][j][0] + acc[0][j][1] + acc[0][j][2];
+    }
+  }
+  if (adapter)
+    nonzeros<RPW, LOCAL>(a, en, ent, k0, kend, beg, end, 0, LOCAL ? 1 : min(a.tp, TB) / 4, zl, ad);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.tokens * 16 * NT; e += kThreads) {
     const int t = e / (16 * NT), n = e % (16 * NT);
-    if (t0 + t >= a.tokens || n0 + n >= a.N) continue;
+    if (n0 + n >= a.N) continue;
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) v += __uint_as_float(own[i][t * LD + n]);
     if (adapter) v = fmaf(a.alpha, ad[n][t], v);
-    Elem<T>::st(y, static_cast<int64_t>(t0 + t) * a.N + n0 + n, v);
+    Elem<T>::st(y, static_cast<int64_t>(t) * a.N + n0 + n, v);
   }
 }
 
-template <int BITS, int S, int MT, int NT, typename T, bool LOCAL>
-hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
+// ---- more tokens: 64 rows of tokens (64 bf16 or 16 fp32 ones) by 128 rows of W
+// per workgroup, a wave 32 of them; the tokens' tiles are staged once for all
+// waves, and the spans are split over `slices` workgroups, whose partial sums
+// decode_finish_kernel adds up.
+constexpr int kWideThreads = 256;
+constexpr int kWideRows = 128;
+constexpr int kWideTiles = 4;
+
+template <int BITS, int MODE, typename T>
+__global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* __restrict__ x,
+                                                                      DecodeArgs a) {
+  constexpr int MT = kWideTiles, NT = 2, G = 1 << MODE;
   constexpr int TB = Rows<T>::TOK * MT;
-  const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.tokens + TB - 1) / TB);
+  constexpr int PX = TB * 16 / kWideThreads;           // pieces of a span per thread
+  using Code = Codes<BITS>;
+  __shared__ __attribute__((aligned(16))) uint32_t tiles[2][MT * kTileWords];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int n0 = blockIdx.x * kWideRows + w * 32, t0 = blockIdx.y * TB;
+  const int spans = (a.K + kSpan - 1) / kSpan;
+  const int first = static_cast<int>(static_cast<int64_t>(spans) * blockIdx.z / a.slices);
+  const int last = static_cast<int>(static_cast<int64_t>(spans) * (blockIdx.z + 1) / a.slices);
+
+  const int nb = min(n0, a.N - 1);                      // waves past N repeat the last row
+  const uint32_t* ctile = a.qw.codes + static_cast<int64_t>(nb) * a.qw.wpr;
+  const float* stile = a.qw.scales + static_cast<int64_t>(nb) * a.qw.gpr;
+  const float* ztile = a.qw.zeros + static_cast<int64_t>(nb) * a.qw.gpr;
+  uint32_t coff[NT], soff[NT], xoff[PX];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int n = min(j * 16 + lr, a.N - 1 - nb);
+    coff[j] = 4u * n * a.qw.wpr;
+    soff[j] = 4u * n * a.qw.gpr;
+  }
+  const int tok = tid >> 4, piece = tid & 15;
+#pragma unroll
+  for (int i = 0; i < PX; ++i)
+    xoff[i] = sizeof(T) * min(t0 + 16 * i + tok, a.tokens - 1) * a.K;
+
+  struct Slot {
+    Code cw[NT];
+    float sc[NT][G], zo[NT][G];
+  } slot[2];
+  Piece<T> xp[PX];
+  auto fetch = [&](Slot& s, int span) {
+    const int c0 = span * kSpan;
+#pragma unroll
+    for (int i = 0; i < PX; ++i) xp[i].load(x, xoff[i], min(c0 + 8 * piece, a.K - 8));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      s.cw[j].load(ctile, coff[j], min(c0 + 32 * lq, a.K - 32));
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int gi = MODE == kWide ? c0 >> a.qw.lg_group : min((c0 >> a.qw.lg_group) + g, a.qw.gpr - 1);
+        s.sc[j][g] = ld_at<float>(stile + gi, soff[j]);
+        s.zo[j][g] = ld_at<float>(ztile + gi, soff[j]);
+      }
+    }
+  };
+  const uint32_t mask = in_vgpr(Code::MASK);
+  const bf16x8 ones = bf16_ones();
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (first < last) fetch(slot[0], first);
+#pragma unroll 1
+  for (int s0 = first; s0 < last; s0 += 2) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int span = s0 + d;
+      if (span >= last) break;
+      // the buffer of the span before the last one: every wave is past the
+      // barrier that follows its reads
+#pragma unroll
+      for (int i = 0; i < PX; ++i) {
+        if constexpr (sizeof(T) == 2)
+          xp[i].store(tiles[d] + i * kTileWords, tok, piece);
+        else
+          xp[i].store(tiles[d] + (tok >> 2) * kTileWords, tok & 3, piece);
+      }
+      if (span + 1 < last) fetch(slot[d ^ 1], span + 1);
+      __syncthreads();
+      span_product<BITS, MODE, MT, NT>(tiles[d], slot[d].cw, slot[d].sc, slot[d].zo,
+                                       a.K - span * kSpan < kSpan, mask, ones, lr, lq, acc);
+    }
+  }
+  float* out = a.part + static_cast<int64_t>(blockIdx.z) * a.tokens * a.N;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + j * 16 + lr;
+      if (n >= a.N) continue;
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = t0 + i * 16 + 4 * lq + r;
+          if (t < a.tokens) out[static_cast<int64_t>(t) * a.N + n] = acc[i][j][r];
+        }
+      } else {
+        const int t = t0 + i * 4 + lq;
+        if (t < a.tokens)
+          out[static_cast<int64_t>(t) * a.N + n] = acc[i][j][0] + acc[i][j][1] + acc[i][j][2];
+      }
+    }
+}
+
+// y = the slices' sums and the nonzeros of 16 rows of F, for up to 64 tokens
+template <typename T>
+__global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
+                                                                 T* __restrict__ y) {
+  constexpr int TB = 64;
+  __shared__ float ad[16][TB + 4];
+  __shared__ uint2 ent[kEntries];
+  const int n0 = blockIdx.x * 16;
+  if (a.row_ptr != nullptr) {
+    const int k0 = a.row_ptr[n0], kend = a.row_ptr[min(n0 + 16, a.N)];
+    const int row = n0 + (threadIdx.x >> 5);
+    const int beg = a.row_ptr[min(row, a.N)], end = a.row_ptr[min(row + 1, a.N)];
+    Entries en;
+    en.load(a, k0, kend);
+    nonzeros<2, false>(a, en, ent, k0, kend, beg, end, 0, a.tp / 4, nullptr, ad);
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e < a.tokens * 16; e += kThreads) {
+    const int t = e >> 4, n = e & 15;
+    if (n0 + n >= a.N) continue;
+    const int64_t at = static_cast<int64_t>(t) * a.N + n0 + n;
+    float v = 0.f;
+    for (int i = 0; i < a.slices; ++i) v += a.part[static_cast<int64_t>(i) * a.tokens * a.N + at];
+    if (a.row_ptr != nullptr) v = fmaf(a.alpha, ad[n][t], v);
+    Elem<T>::st(y, at, v);
+  }
+}
+
+// ---- launches
+template <int BITS, int MODE, int NT, typename T, bool FEW, bool LOCAL>
+hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
+  const dim3 grid((a.N + 16 * NT - 1) / (16 * NT));
   const size_t lds = LOCAL ? static_cast<size_t>(a.tokens) * (a.K + a.K / 16) * 4 : 0;
-  hipLaunchKernelGGL((decode_kernel<BITS, S, MT, NT, T, LOCAL>), grid, dim3(kThreads), lds, s, x, a,
-                     y);
+  hipLaunchKernelGGL((decode_kernel<BITS, MODE, NT, T, FEW, LOCAL>), grid, dim3(kThreads), lds, s,
+                     x, a, y);
   return hipGetLastError();
 }
 
 // tokens few enough for the transform in LDS
 bool is_local(int T, int K) { return T <= kLocalTokens && T * K <= kLocal; }
 
-template <int BITS, int S, typename T>
-hipError_t decode_s(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
-  if (a.row_ptr != nullptr && is_local(a.tokens, a.K))
-    return decode_t<BITS, S, 1, 1, T, true>(x, a, y, s);
-  const int tiles = (a.tokens + Rows<T>::TOK - 1) / Rows<T>::TOK;
-  if (tiles == 1)
-    return a.N >= 8192 ? decode_t<BITS, S, 1, 2, T, false>(x, a, y, s)
-                       : decode_t<BITS, S, 1, 1, T, false>(x, a, y, s);
-  if (tiles == 2) return decode_t<BITS, S, 2, 1, T, false>(x, a, y, s);
-  return decode_t<BITS, S, 4, 1, T, false>(x, a, y, s);
+template <int BITS, int MODE, typename T>
+hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
+  if (a.tokens > Rows<T>::TOK) {
+    constexpr int TB = Rows<T>::TOK * kWideTiles;
+    const dim3 grid((a.N + kWideRows - 1) / kWideRows, (a.tokens + TB - 1) / TB, a.slices);
+    hipLaunchKernelGGL((decode_wide_kernel<BITS, MODE, T>), grid, dim3(kWideThreads), 0, s, x, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((decode_finish_kernel<T>), dim3((a.N + 15) / 16), dim3(kThreads), 0, s, a, y);
+    return hipGetLastError();
+  }
+  if (a.tokens <= 4) {
+    if (a.row_ptr != nullptr && is_local(a.tokens, a.K))
+      return decode_t<BITS, MODE, 1, T, true, true>(x, a, y, s);
+    return decode_t<BITS, MODE, 1, T, true, false>(x, a, y, s);
+  }
+  if constexpr (sizeof(T) == 2) {
+    return a.N >= 8192 ? decode_t<BITS, MODE, 2, T, false, false>(x, a, y, s)
+                       : decode_t<BITS, MODE, 1, T, false, false>(x, a, y, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <int BITS, typename T>
 hipError_t decode_b(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
-  if (a.qw.lg_group == 5) return decode_s<BITS, 1, T>(x, a, y, s);
-  if (a.qw.lg_group == 6) return decode_s<BITS, 2, T>(x, a, y, s);
-  return decode_s<BITS, 4, T>(x, a, y, s);
+  if (a.qw.lg_group == 5) return decode_m<BITS, kFull, T>(x, a, y, s);
+  if (a.qw.lg_group == 6) return decode_m<BITS, kHalf, T>(x, a, y, s);
+  return decode_m<BITS, kWide, T>(x, a, y, s);
 }
 
 template <typename T>
@@ -680,29 +849,6 @@ hipError_t decode_d(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   }
 }
 
-template <int LOG_N, typename T>
-hipError_t fwht_t(const T* x, int tokens, int nblk, int tp, float* zt, hipStream_t s) {
-  using Z = Zt<LOG_N>;
-  const dim3 grid((nblk + Z::BLKS - 1) / Z::BLKS, (tokens + Z::TT - 1) / Z::TT);
-  hipLaunchKernelGGL((decode_fwht_kernel<LOG_N, T>), grid, dim3(Z::BLOCK), 0, s, x, tokens, nblk,
-                     tp, zt);
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t fwht_d(const T* x, int tokens, int log_n, int nblk, int tp, float* zt, hipStream_t s) {
-  switch (log_n) {
-#define QWHA_CASE(L) \
-  case L:            \
-    return fwht_t<L, T>(x, tokens, nblk, tp, zt, s);
-    QWHA_CASE(6) QWHA_CASE(7) QWHA_CASE(8) QWHA_CASE(9) QWHA_CASE(10) QWHA_CASE(11)
-    QWHA_CASE(12) QWHA_CASE(13) QWHA_CASE(14)
-#undef QWHA_CASE
-    default:
-      return hipErrorInvalidValue;
-  }
-}
-
 // tokens a column of zt holds: a power of two, 4 at least
 int padded_tokens(int T) {
   int tp = 4;
@@ -710,12 +856,29 @@ int padded_tokens(int T) {
   return tp;
 }
 
+// Workgroups that share the spans of 128 rows: enough of them for two per
+// compute unit, at least two spans each.
+int wide_slices(int K, int N) {
+  const int tiles = (N + kWideRows - 1) / kWideRows, spans = (K + kSpan - 1) / kSpan;
+  const int want = (512 + tiles - 1) / tiles, most = spans / 2 > 0 ? spans / 2 : 1;
+  return want < most ? want : most;
+}
+
+struct DecodeWs {
+  size_t part, total;     // zt at 0
+};
+DecodeWs decode_ws(int T, int K, int N, int64_t p) {
+  DecodeWs l;
+  l.part = p > 0 && !is_local(T, K) ? static_cast<size_t>(K) * padded_tokens(T) * 4 : 0;
+  l.total = l.part;
+  // fp32 calls take the wide kernel from 5 tokens on, bf16 ones from 17
+  if (T > Rows<float>::TOK) l.total += static_cast<size_t>(wide_slices(K, N)) * T * N * 4;
+  return l;
+}
+
 }  // namespace
 
-size_t decode_scratch_bytes(int64_t T, int K, int64_t p) {
-  if (p == 0 || is_local(static_cast<int>(T), K)) return 0;
-  return static_cast<size_t>(K) * padded_tokens(static_cast<int>(T)) * 4;
-}
+size_t decode_scratch_bytes(int T, int K, int N, int64_t p) { return decode_ws(T, K, N, p).total; }
 
 hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N,
                          const QuantW& qw, int64_t p, const int32_t* row_ptr, const int32_t* E,
@@ -726,20 +889,20 @@ hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N
   a.N = N;
   a.tp = padded_tokens(T);
   a.qw = qw;
-  a.zt = nullptr;
   a.row_ptr = p > 0 ? row_ptr : nullptr;
   a.E = E;
   a.c = c;
-  a.alpha = alpha;
   a.log_b = log_n;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + decode_ws(T, a.K, N, p).part);
+  a.slices = wide_slices(a.K, N);
   const bool through_memory = p > 0 && !is_local(T, a.K);
-  if (through_memory)
-    a.zt = static_cast<float*>(scratch);
-  else
-    a.alpha = alpha / static_cast<float>(1 << log_n);
+  a.zt = through_memory ? static_cast<float*>(scratch) : nullptr;
+  a.alpha = through_memory ? alpha : alpha / static_cast<float>(1 << log_n);
   auto go = [&](auto* xx, auto* yy) {
     if (through_memory) {
-      const hipError_t e = fwht_d(xx, T, log_n, nblk, a.tp, static_cast<float*>(scratch), s);
+      hipLaunchKernelGGL((decode_z_kernel<std::remove_const_t<std::remove_pointer_t<decltype(yy)>>>), dim3(T), dim3(kThreads), (a.K + a.K / 16) * sizeof(float),
+                         s, xx, a.K, log_n, a.tp, static_cast<float*>(scratch));
+      const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     return decode_d(xx, a, yy, s);

@@ -82,7 +82,7 @@ hipError_t launch_qgemm(const uint16_t* x, int64_t T, int K, int N, const QuantW
 
 // y = x W_Q^T + alpha z F^T for T <= 64 tokens of K = nblk * 2^log_n columns
 // (decode.hip); p = 0: no adapter, row_ptr, E, c and scratch are not used
-size_t decode_scratch_bytes(int64_t T, int K, int64_t p);
+size_t decode_scratch_bytes(int T, int K, int N, int64_t p);
 hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N,
                          const QuantW& qw, int64_t p, const int32_t* row_ptr, const int32_t* E,
                          const float* c, float alpha, void* y, void* scratch, hipStream_t s);
