@@ -724,10 +724,11 @@ size_t qwha_cache_attn_workspace_bytes(int32_t B, int32_t q_heads, int32_t heads
                                        int32_t head_dim, int32_t width, int32_t page) {
   if (B < 0 || B > 65535 || heads < 1 || heads > 4096 || q_heads < 1 || q_heads > 65535 ||
       q_heads % heads != 0 || width < 1 || page < 8 || page > 1024 ||
+      static_cast<int64_t>(width) * page > INT32_MAX ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   return align256(cache_attn_scratch_bytes(B, q_heads, heads, head_dim,
-                                           static_cast<int64_t>(width) * page));
+                                           static_cast<int64_t>(width) * page, page));
 }
 
 qwha_status qwha_cache_attn(const void* q, qwha_dtype act, int32_t B, int32_t q_heads,

@@ -30,8 +30,25 @@ struct Cache {
   }
 };
 
+// Calls fn with the kernel's compile-time choices.
+template <typename Fn>
+hipError_t by_shape(int dim, int bits, Fn&& fn) {
+  using std::integral_constant;
+  if (bits == 4) {
+    if (dim == 64) return fn(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    if (dim == 128) return fn(integral_constant<int, 128>{}, integral_constant<int, 4>{});
+    if (dim == 256) return fn(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  } else if (bits == 8) {
+    if (dim == 64) return fn(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    if (dim == 128) return fn(integral_constant<int, 128>{}, integral_constant<int, 8>{});
+    if (dim == 256) return fn(integral_constant<int, 256>{}, integral_constant<int, 8>{});
+  }
+  return hipErrorInvalidValue;
+}
+
 // q_heads / heads query heads read each head; max_tokens = width * page
-size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t max_tokens);
+size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t max_tokens,
+                                int page);
 hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,
                               const int32_t* slots, int rotate, const Cache& c, hipStream_t s);
 hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, int rotate, Dt dt,

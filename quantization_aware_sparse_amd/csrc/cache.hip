@@ -1,4 +1,5 @@
-// The quantized key/value cache: rows written, read back, and attended to.
+// The quantized key/value cache: rows written and read back (attention over
+// them: cache_attn.hip).
 //
 // A row is the head_dim values of one token's key or value of one head. With
 // the transform on, what is stored is v = fp32(x H / n), n = head_dim, H the
@@ -9,39 +10,11 @@
 //   z = floor(-lo/s + 1/2), q = clip(floor(v/s + 1/2) + z, 0, 2^b - 1),
 // and read back as x' = s (q - z) H.
 #include "cache.h"
+#include "lane_fwht.h"
 
 namespace qwha {
 
 namespace {
-
-// Lanes of a row hold 16 consecutive columns each; N / 16 lanes a row.
-template <int X, typename Acc>
-__device__ __forceinline__ void butterfly_lanes(Acc* v, int lane) {
-  const bool upper = (lane & X) != 0;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const Acc o = lane_xor<X>(v[r]);
-    v[r] = upper ? o - v[r] : v[r] + o;
-  }
-}
-
-// v H over N columns, 16 a lane
-template <int N, typename Acc>
-__device__ __forceinline__ void fwht_lanes(Acc* v, int lane) {
-#pragma unroll
-  for (int h = 1; h < 16; h <<= 1)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      if (r & h) continue;
-      const Acc a = v[r], c = v[r + h];
-      v[r] = a + c;
-      v[r + h] = a - c;
-    }
-  if constexpr (N > 16) butterfly_lanes<1>(v, lane);
-  if constexpr (N > 32) butterfly_lanes<2>(v, lane);
-  if constexpr (N > 64) butterfly_lanes<4>(v, lane);
-  if constexpr (N > 128) butterfly_lanes<8>(v, lane);
-}
 
 template <int N, bool MAX>
 __device__ __forceinline__ float row_extreme(float m) {
@@ -140,24 +113,6 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict_
   }
 }
 
-template <typename TOut>
-__device__ __forceinline__ void store16(TOut* dst, const float* f) {
-  if constexpr (sizeof(TOut) == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<float4*>(dst)[i] = float4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = static_cast<uint32_t>(f32_to_bf16(f[2 * i])) |
-             (static_cast<uint32_t>(f32_to_bf16(f[2 * i + 1])) << 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      reinterpret_cast<uint4*>(dst)[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
-  }
-}
-
 // Rows [T][2][heads] of the slots, dense; a token without a slot reads as
 // zeros. Bound by HBM's writes: head_dim elements out for head_dim * b / 8 + 8
 // bytes in.
@@ -200,121 +155,6 @@ __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
   // every lane of a row takes the same branch above, so the butterflies see whole rows
   if constexpr (ROT) fwht_lanes<N>(f, u);
   if (live) store16((part ? v : k) + (t * c.heads + h) * N + u * 16, f);
-}
-
-// One workgroup per (sequence, query head); tokens in tiles of 256, one a
-// thread for the scores, then the head's columns over the threads for the
-// values, with the running maximum and sum of the softmax.
-template <int N, int BITS, typename T>
-__global__ __launch_bounds__(256) void cache_attn_kernel(const T* __restrict__ q, Cache c,
-                                                         int q_heads,
-                                                         const int32_t* __restrict__ table,
-                                                         int width,
-                                                         const int32_t* __restrict__ lens,
-                                                         float scale, int rotate,
-                                                         T* __restrict__ out) {
-  constexpr int CPW = 32 / BITS;
-  constexpr int PARTS = 256 / N;       // token subsets the value sums are split over
-  __shared__ float qs[N], acc_s[256], red[256], ps[256];
-  __shared__ int64_t rows[256];
-  const int b = blockIdx.y, hq = blockIdx.x, tid = threadIdx.x;
-  const int h = hq / (q_heads / c.heads);
-  auto turn = [&](float* a) {          // a <- a H in LDS
-    for (int w = 1; w < N; w <<= 1) {
-      __syncthreads();
-      if (tid < N / 2) {
-        const int i = (tid / w) * 2 * w + tid % w;
-        const float x = a[i], y = a[i + w];
-        a[i] = x + y;
-        a[i + w] = x - y;
-      }
-    }
-    __syncthreads();
-  };
-  const int64_t qrow = static_cast<int64_t>(b) * q_heads + hq;
-  if (tid < N) qs[tid] = Elem<T>::ld(q, qrow * N + tid);
-  if (rotate) turn(qs);
-  __syncthreads();
-  int64_t len = lens[b];
-  if (len > (static_cast<int64_t>(width) << c.lg_page)) len = static_cast<int64_t>(width) << c.lg_page;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int64_t t0 = 0; t0 < len; t0 += 256) {
-    const int64_t t = t0 + tid;
-    float a = -INFINITY;
-    int64_t at = -1;
-    if (t < len) {
-      const int32_t pg = table[static_cast<int64_t>(b) * width + (t >> c.lg_page)];
-      if (pg >= 0 && pg < c.n_pages) {
-        at = c.row_in(0, pg, static_cast<int>(t & ((1 << c.lg_page) - 1)), h);
-        const uint32_t* w = c.codes + at * (N / CPW);
-        const float z = c.zeros[at];
-        float d = 0.f;
-        for (int i = 0; i < N / CPW; ++i)
-          for (int e = 0; e < CPW; ++e)
-            d += qs[i * CPW + e] *
-                 (static_cast<float>((w[i] >> (e * BITS)) & ((1u << BITS) - 1u)) - z);
-        a = d * c.scales[at] * scale;
-      }
-    }
-    rows[tid] = at;
-    red[tid] = a;
-    __syncthreads();
-    for (int w = 128; w > 0; w >>= 1) {
-      if (tid < w) red[tid] = fmaxf(red[tid], red[tid + w]);
-      __syncthreads();
-    }
-    const float mn = fmaxf(m, red[0]);
-    __syncthreads();
-    const float p = at >= 0 ? expf(a - mn) : 0.f;
-    ps[tid] = p;
-    red[tid] = p;
-    __syncthreads();
-    for (int w = 128; w > 0; w >>= 1) {
-      if (tid < w) red[tid] += red[tid + w];
-      __syncthreads();
-    }
-    const float keep = mn > -INFINITY ? expf(m - mn) : 1.f;
-    l = l * keep + red[0];
-    acc *= keep;
-    m = mn;
-    const int col = tid % N;
-    const int64_t vals = c.part_rows();
-    for (int i = tid / N; i < 256; i += PARTS) {
-      const int64_t r = rows[i];
-      if (r < 0) continue;
-      const int64_t vr = r + vals;
-      const uint32_t w = c.codes[vr * (N / CPW) + col / CPW];
-      const float x = static_cast<float>((w >> ((col % CPW) * BITS)) & ((1u << BITS) - 1u));
-      acc += ps[i] * ((x - c.zeros[vr]) * c.scales[vr]);
-    }
-    __syncthreads();
-  }
-  acc_s[tid] = acc;
-  __syncthreads();
-  if (tid < N) {
-    float o = 0.f;
-    for (int i = 0; i < PARTS; ++i) o += acc_s[i * N + tid];
-    qs[tid] = l > 0.f ? o / l : 0.f;
-  }
-  if (rotate) turn(qs);
-  __syncthreads();
-  if (tid < N) Elem<T>::st(out, qrow * N + tid, qs[tid]);
-}
-
-// Calls fn with the kernel's compile-time choices.
-template <typename Fn>
-hipError_t by_shape(int dim, int bits, Fn&& fn) {
-  using std::integral_constant;
-  if (bits == 4) {
-    if (dim == 64) return fn(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-    if (dim == 128) return fn(integral_constant<int, 128>{}, integral_constant<int, 4>{});
-    if (dim == 256) return fn(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-  } else if (bits == 8) {
-    if (dim == 64) return fn(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-    if (dim == 128) return fn(integral_constant<int, 128>{}, integral_constant<int, 8>{});
-    if (dim == 256) return fn(integral_constant<int, 256>{}, integral_constant<int, 8>{});
-  }
-  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -362,26 +202,6 @@ hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, in
     auto* vv = static_cast<uint16_t*>(v);
     return rotate ? go(cache_read_kernel<N, BITS, uint16_t, true>, kk, vv)
                   : go(cache_read_kernel<N, BITS, uint16_t, false>, kk, vv);
-  });
-}
-
-size_t cache_attn_scratch_bytes(int, int, int, int, int64_t) { return 0; }
-
-hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cache& c,
-                             const int32_t* table, int width, const int32_t* lens, float scale,
-                             int rotate, void* out, void*, hipStream_t s) {
-  return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
-    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
-    const dim3 grid(static_cast<unsigned>(q_heads), static_cast<unsigned>(B));
-    if (dt == Dt::F32)
-      hipLaunchKernelGGL((cache_attn_kernel<N, BITS, float>), grid, dim3(256), 0, s,
-                         static_cast<const float*>(q), c, q_heads, table, width, lens, scale,
-                         rotate, static_cast<float*>(out));
-    else
-      hipLaunchKernelGGL((cache_attn_kernel<N, BITS, uint16_t>), grid, dim3(256), 0, s,
-                         static_cast<const uint16_t*>(q), c, q_heads, table, width, lens, scale,
-                         rotate, static_cast<uint16_t*>(out));
-    return hipGetLastError();
   });
 }
 

@@ -1,0 +1,486 @@
+// Attention of one query token per sequence over the quantized cache:
+//   out = sum_t softmax_t(scale q . k_t) v_t,  k_t = s (code - z) H (H = 1
+// without the transform). H is symmetric, so q . k_t = (q H) . (s (code - z)):
+// the query is transformed once instead of every key, and the sum over the
+// values' codes once instead of every value.
+//
+// A workgroup takes one key/value head of one sequence, up to 4 HT of the query
+// heads that read it, and a slice of the tokens; its waves take tiles of 32
+// tokens in turn, each with its own running maximum and sum of the softmax.
+// Both products run on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16):
+//   scores  A: 16 rows = 4 query heads x (upper, middle, lower 8 bits of the
+//           fp32 query's mantissa, nothing); B: 16 tokens' codes. Lane l holds
+//           token l % 16 and a quarter of its row;
+//   values  A: the weights p s_v, split alike; B: for each of N / 16 columns j
+//           the codes of column (N / 16) (l % 16) + j of 8 tokens: a lane reads
+//           its N / 16 columns of 8 tokens and pairs the tokens' codes up.
+// Codes enter as 2^bits + q (4 bits) or q (8 bits), all exact in bf16, and the
+// rest of (q - z) is taken off in fp32: with OFF = 16 or 0
+//   score   = s_k (sum q' (OFF + code) - (OFF + z_k) sum q'),
+//   output  = sum p s_v (OFF + code) - sum p s_v (OFF + z_v).
+// So every product is exact and only fp32 additions round. The three parts of a
+// head lie in one lane's results.
+//
+// cache_combine_kernel joins the slices: one maximum, one sum, one transform.
+#include "cache.h"
+#include "lane_fwht.h"
+#include "mfma_codes.h"
+
+namespace qwha {
+
+namespace {
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnThreads = kAttnWaves * 64;
+constexpr int kTile = 32;                           // tokens
+constexpr int kTabPages = 1024;                     // pages a slice holds, at most
+constexpr int kTab = kTabPages + kAttnWaves * kTile / 8 + 1;
+
+struct AttnArgs {
+  int q_heads, per, groups;    // query heads per key/value head, in groups of 4 HT
+  const int32_t* table;
+  int width;
+  const int32_t* lens;
+  float scale;                 // times log2 e: the softmax runs on powers of two
+  int rotate, slices;
+  float* part;                 // [B][q_heads][slices][N]
+  float2* ml;                  // [B][q_heads][slices]: maximum, sum
+};
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// over the 16 lanes of a quarter
+__device__ __forceinline__ float quarter_max(float v) {
+  v = fmaxf(v, lane_xor<1>(v));
+  v = fmaxf(v, lane_xor<2>(v));
+  v = fmaxf(v, lane_xor<4>(v));
+  return fmaxf(v, lane_xor<8>(v));
+}
+__device__ __forceinline__ float quarter_sum(float v) {
+  v += lane_xor<1>(v);
+  v += lane_xor<2>(v);
+  v += lane_xor<4>(v);
+  return v + lane_xor<8>(v);
+}
+
+// part `r` (0: upper, 1: middle, 2: lower, 3: nothing) of 8 fp32 numbers
+__device__ __forceinline__ bf16x8 part_operand(const float* f, int r) {
+  uint32_t x[8], d[4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h[3];
+    split3(f[i], h);
+    x[i] = r == 0 ? h[0] : r == 1 ? h[1] : r == 2 ? h[2] : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
+  return as_operand(d);
+}
+
+template <int WORDS>
+__device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
+  if constexpr (WORDS >= 4) {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// o[N] in LDS -> out, through the transform: N / 16 lanes
+template <int N, typename T>
+__device__ __forceinline__ void finish_row(const float* o, int u, int rotate, T* out) {
+  float v[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) v[r] = o[u * 16 + r];
+  if (rotate) fwht_lanes<N>(v, u);
+  store16(out + u * 16, v);
+}
+
+template <int N, int BITS, int HT, typename T>
+__global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __restrict__ q,
+                                                                     Cache c, AttnArgs a,
+                                                                     T* __restrict__ out) {
+  constexpr int HEADS = 4 * HT;
+  constexpr int STEPS = N / 32;                     // matrix instructions of a score
+  constexpr int KW = N / 4 * BITS / 32;             // words of a quarter of a row
+  constexpr int J = N / 16;                         // columns of a lane
+  constexpr int VB = J * BITS / 8;                  // bytes of them
+  constexpr int VW = VB >= 4 ? VB / 4 : 1;
+  constexpr int ROW = N * BITS / 8;                 // bytes of a row
+  constexpr float OFF = BITS == 4 ? 16.f : 0.f;
+  constexpr int PLD = kTile + 4;
+  __shared__ __attribute__((aligned(16))) float qs[HEADS][N];
+  __shared__ __attribute__((aligned(16))) float om[kAttnWaves][HEADS][N];
+  __shared__ float2 wml[kAttnWaves][HEADS];
+  __shared__ int32_t tab[kTab];
+  float (*ps)[4][PLD] = reinterpret_cast<float (*)[4][PLD]>(&om[threadIdx.x >> 6][0][0]);
+  static_assert(HT * 4 * PLD <= HEADS * N, "a wave's weights fit its place for results");
+
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int b = blockIdx.y;
+  const int slice = blockIdx.x % a.slices, hg = blockIdx.x / a.slices;
+  const int h = hg / a.groups, h0 = hg % a.groups * HEADS;     // key/value head, first query head
+  const int heads = min(HEADS, a.per - h0);
+  const int64_t qrow = static_cast<int64_t>(b) * a.q_heads + static_cast<int64_t>(h) * a.per + h0;
+
+  const int64_t cap = static_cast<int64_t>(a.width) << c.lg_page;
+  const int64_t asked = a.lens[b];
+  const uint32_t len = static_cast<uint32_t>(asked < 0 ? 0 : asked < cap ? asked : cap);
+  const uint32_t tiles = (len + kTile - 1) / kTile;
+  uint32_t each = (tiles + a.slices - 1) / a.slices;
+  each = (each + kAttnWaves - 1) & ~(kAttnWaves - 1u);
+  const uint32_t first = min(static_cast<uint64_t>(slice) * each, static_cast<uint64_t>(tiles));
+  const uint32_t last = min(first + each, tiles);
+
+  // the slice's pages; one outside the cache, and those behind the sequence, as -1
+  const uint32_t p0 = (first * kTile) >> c.lg_page;
+  {
+    const uint32_t pages = (len + (1u << c.lg_page) - 1) >> c.lg_page;
+    const uint32_t p1 = (last * kTile + (1u << c.lg_page) - 1) >> c.lg_page;
+    const int32_t* row = a.table + static_cast<int64_t>(b) * a.width;
+    for (uint32_t p = p0 + tid; p < p1; p += kAttnThreads) {
+      const int32_t g = p < pages ? row[p] : -1;
+      tab[p - p0] = g >= 0 && g < c.n_pages ? g : -1;
+    }
+  }
+  if (tid < HEADS * J) {                            // one wave, N / 16 lanes a head
+    const int head = tid / J, u = tid % J;
+    float v[16];
+    load16(q + (qrow + min(head, heads - 1)) * N + u * 16, v);
+    if (a.rotate) fwht_lanes<N>(v, u);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) qs[head][u * 16 + r] = v[r] * a.scale;
+  }
+  __syncthreads();
+
+  bf16x8 qf[HT][STEPS];
+  float qsum[HT];
+#pragma unroll
+  for (int t = 0; t < HT; ++t) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 8 + i];
+      qf[t][s] = part_operand(f, lr & 3);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < J; ++i) sum += qs[t * 4 + lq][lr * J + i];
+    qsum[t] = quarter_sum(sum);
+  }
+
+  const uint32_t mask = in_vgpr(kMask4);
+  const f32x4 zero4 = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t vals = c.part_rows();
+  const uint32_t in_page = (1u << c.lg_page) - 1;
+  f32x4 acc[HT][J];
+  float m[HT], l[HT], zacc[HT];
+#pragma unroll
+  for (int t = 0; t < HT; ++t) {
+    m[t] = -INFINITY;
+    l[t] = 0.f;
+    zacc[t] = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[t][j] = zero4;
+  }
+
+  struct Tile {
+    uint32_t k[2][KW], v[8][VW];
+    float sk[2], zk[2], sv[2], zv[2];
+    bool live[2];
+  };
+  auto row_of = [&](uint32_t t, bool* live) {       // clamped to the cache's first page
+    const int32_t g = tab[(t >> c.lg_page) - p0];
+    *live = t < len && g >= 0;
+    return c.row_in(0, g < 0 ? 0 : g, static_cast<int>(t & in_page), h);
+  };
+  auto fetch = [&](Tile& x, uint32_t tile) {
+    const char* codes = reinterpret_cast<const char*>(c.codes);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = row_of(tile * kTile + 16 * i + lr, &x.live[i]);
+      load_words<KW>(codes + r * ROW + lq * (ROW / 4), x.k[i]);
+      x.sk[i] = c.scales[r];
+      x.zk[i] = c.zeros[r];
+      x.sv[i] = c.scales[vals + r];
+      x.zv[i] = c.zeros[vals + r];
+    }
+    // 8 tokens of one page (8 divides the page)
+    bool any;
+    const char* vp = codes + (vals + row_of(tile * kTile + 8 * lq, &any)) * ROW + lr * VB;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (VB >= 4)
+        load_words<VW>(vp + i * ROW, x.v[i]);
+      else
+        x.v[i][0] = *reinterpret_cast<const uint16_t*>(vp + i * ROW);
+    }
+  };
+
+  Tile cur;
+  if (first + w < last) fetch(cur, first + w);
+#pragma unroll 1
+  for (uint32_t tile = first + w; tile < last; tile += kAttnWaves) {
+    Tile next;
+    if (tile + kAttnWaves < last) fetch(next, tile + kAttnWaves);
+
+    f32x4 sg[HT][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        bf16x8 kf;
+        if constexpr (BITS == 4)
+          kf = operand4(cur.k[i][s], mask);
+        else
+          kf = operand8(cur.k[i][2 * s], cur.k[i][2 * s + 1]);
+#pragma unroll
+        for (int t = 0; t < HT; ++t)
+          sg[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[t][s], kf, s ? sg[t][i] : zero4, 0, 0, 0);
+      }
+    // what lies in a place that is left out is never used, whatever it holds
+    float sv[2], ov[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sv[i] = cur.live[i] ? cur.sv[i] : 0.f;
+      ov[i] = cur.live[i] ? OFF + cur.zv[i] : 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < HT; ++t) {
+      float s[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float d = sg[t][i][0] + sg[t][i][1] + sg[t][i][2];
+        const float x = cur.sk[i] * fmaf(-(OFF + cur.zk[i]), qsum[t], d);
+        s[i] = cur.live[i] ? x : -INFINITY;
+      }
+      const float mn = fmaxf(m[t], quarter_max(fmaxf(s[0], s[1])));
+      const float at = mn == -INFINITY ? 0.f : mn;    // nothing to see yet: all weights are 0
+      if (__any(mn > m[t])) {
+        const float keep = exp2_fast(m[t] - at);
+        l[t] *= keep;
+        zacc[t] *= keep;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[t][j][r] *= keep;
+        m[t] = mn;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float p = exp2_fast(s[i] - at);
+        l[t] += p;
+        const float pv = p * sv[i];
+        zacc[t] = fmaf(pv, ov[i], zacc[t]);
+        ps[t][lq][16 * i + lr] = pv;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    bf16x8 pf[HT];
+#pragma unroll
+    for (int t = 0; t < HT; ++t) {
+      const float4* p = reinterpret_cast<const float4*>(&ps[t][lr >> 2][8 * lq]);
+      const float4 p0v = p[0], p1v = p[1];
+      const float f[8] = {p0v.x, p0v.y, p0v.z, p0v.w, p1v.x, p1v.y, p1v.z, p1v.w};
+      pf[t] = part_operand(f, lr & 3);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      uint32_t d[4];
+      if constexpr (BITS == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = cur.v[2 * k][j / 8], hi = cur.v[2 * k + 1][j / 8];
+          const uint32_t sel = 0x0C040C00u + 0x00010001u * (j % 8 / 2);
+          d[k] = j % 2 ? and_or(__builtin_amdgcn_perm(hi >> 1, lo >> 1, sel), mask, kBase4)
+                       : and_or(__builtin_amdgcn_perm(hi << 3, lo << 3, sel), mask, kBase4);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          d[k] = __builtin_amdgcn_perm(byte_f32(cur.v[2 * k + 1][j / 4], j % 4),
+                                       byte_f32(cur.v[2 * k][j / 4], j % 4), 0x07060302u);
+      }
+      const bf16x8 vf = as_operand(d);
+#pragma unroll
+      for (int t = 0; t < HT; ++t)
+        acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[t], vf, acc[t][j], 0, 0, 0);
+    }
+    cur = next;
+  }
+
+  // the waves' sums, joined
+#pragma unroll
+  for (int t = 0; t < HT; ++t) {
+    const float zs = quarter_sum(zacc[t]), ls = quarter_sum(l[t]);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      om[w][t * 4 + lq][lr * J + j] = acc[t][j][0] + acc[t][j][1] + acc[t][j][2] - zs;
+    if (lr == 0) wml[w][t * 4 + lq] = float2{m[t], ls};
+  }
+  __syncthreads();
+  for (int e = tid; e < heads * N; e += kAttnThreads) {
+    const int head = e / N, d = e % N;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kAttnWaves; ++i) top = fmaxf(top, wml[i][head].x);
+    float o = 0.f, sum = 0.f;
+    if (top > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < kAttnWaves; ++i) {
+        const float f = exp2_fast(wml[i][head].x - top);
+        o = fmaf(f, om[i][head][d], o);
+        sum = fmaf(f, wml[i][head].y, sum);
+      }
+    }
+    if (a.slices == 1) {
+      qs[head][d] = sum > 0.f ? o / sum : 0.f;
+    } else {
+      const int64_t at = (qrow + head) * a.slices + slice;
+      a.part[at * N + d] = o;
+      if (d == 0) a.ml[at] = float2{top, sum};
+    }
+  }
+  if (a.slices == 1) {
+    __syncthreads();
+    if (tid < heads * J) finish_row<N>(qs[tid / J], tid % J, a.rotate, out + (qrow + tid / J) * N);
+  }
+}
+
+// One query head of one sequence: its slices, joined. N / 16 lanes hold a
+// slice's sums; the workgroup's 16 * 256 / N such groups take the slices in turn.
+template <int N, typename T>
+__global__ __launch_bounds__(kAttnThreads) void cache_combine_kernel(AttnArgs a,
+                                                                     T* __restrict__ out) {
+  constexpr int J = N / 16, GROUPS = kAttnThreads / J;
+  __shared__ float os[GROUPS][N + 4];
+  __shared__ float tops[kAttnWaves], sums[GROUPS];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, u = tid % J, g = tid / J;
+  const float2* ml = a.ml + row * a.slices;
+  float top = -INFINITY;
+  for (int s = tid; s < a.slices; s += kAttnThreads) top = fmaxf(top, ml[s].x);
+  top = quarter_max(top);
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  if ((tid & 63) == 0) tops[tid >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAttnWaves; ++i) top = fmaxf(top, tops[i]);
+  float v[16], sum = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) v[r] = 0.f;
+  if (top > -INFINITY) {
+    for (int s = g; s < a.slices; s += GROUPS) {
+      const float2 x = ml[s];
+      if (!(x.y > 0.f)) continue;                  // a slice without tokens
+      const float f = exp2_fast(x.x - top);
+      sum = fmaf(f, x.y, sum);
+      const float4* p = reinterpret_cast<const float4*>(a.part + (row * a.slices + s) * N + u * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 o = p[i];
+        v[4 * i] = fmaf(f, o.x, v[4 * i]);
+        v[4 * i + 1] = fmaf(f, o.y, v[4 * i + 1]);
+        v[4 * i + 2] = fmaf(f, o.z, v[4 * i + 2]);
+        v[4 * i + 3] = fmaf(f, o.w, v[4 * i + 3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) os[g][u * 16 + r] = v[r];
+  if (u == 0) sums[g] = sum;
+  __syncthreads();
+  const int used = min(GROUPS, a.slices);
+  if (tid < N) {
+    float o = 0.f, l = 0.f;
+    for (int i = 0; i < used; ++i) {
+      o += os[i][tid];
+      l += sums[i];
+    }
+    os[0][tid] = l > 0.f ? o / l : 0.f;
+  }
+  __syncthreads();
+  if (tid < J) finish_row<N>(os[0], u, a.rotate, out + row * N);
+}
+
+// Query heads of a workgroup: tiles of 4, two of them where there are more than
+// 4 and the columns leave the registers for it.
+int head_tiles(int per, int dim) { return per > 4 && dim <= 128 ? 2 : 1; }
+
+// Slices of a sequence: workgroups for four per compute unit, each with a tile
+// for every wave, and no more pages than its table holds.
+int attn_slices(int B, int q_heads, int heads, int dim, int64_t max_tokens, int page) {
+  const int per = q_heads / heads, ht = head_tiles(per, dim);
+  const int64_t groups = (per + 4 * ht - 1) / (4 * ht);
+  const int64_t pairs = static_cast<int64_t>(B) * heads * groups;
+  const int64_t most = (max_tokens + kAttnWaves * kTile - 1) / (kAttnWaves * kTile);
+  const int64_t least = (max_tokens + kTabPages * static_cast<int64_t>(page) - 1) /
+                        (kTabPages * static_cast<int64_t>(page));
+  int64_t want = pairs > 0 ? (1024 + pairs - 1) / pairs : 1;
+  if (want > most) want = most;
+  if (want < least) want = least;
+  return static_cast<int>(want < 1 ? 1 : want);
+}
+
+}  // namespace
+
+size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t max_tokens,
+                                int page) {
+  const int slices = attn_slices(B, q_heads, heads, dim, max_tokens, page);
+  if (slices == 1) return 0;
+  return static_cast<size_t>(B) * q_heads * slices * (dim + 2) * sizeof(float);
+}
+
+hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cache& c,
+                             const int32_t* table, int width, const int32_t* lens, float scale,
+                             int rotate, void* out, void* scratch, hipStream_t s) {
+  AttnArgs a;
+  a.q_heads = q_heads;
+  a.per = q_heads / c.heads;
+  const int ht = head_tiles(a.per, c.dim);
+  a.groups = (a.per + 4 * ht - 1) / (4 * ht);
+  a.table = table;
+  a.width = width;
+  a.lens = lens;
+  a.scale = scale * 1.44269504088896340736f;
+  a.rotate = rotate;
+  a.slices = attn_slices(B, q_heads, c.heads, c.dim, static_cast<int64_t>(width) << c.lg_page,
+                         1 << c.lg_page);
+  a.part = static_cast<float*>(scratch);
+  a.ml = reinterpret_cast<float2*>(a.part + static_cast<int64_t>(B) * q_heads * a.slices * c.dim);
+  const dim3 grid(static_cast<unsigned>(c.heads) * a.groups * a.slices, static_cast<unsigned>(B));
+  return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
+    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
+    auto go = [&](auto* qq, auto* oo) {
+      using T = std::remove_pointer_t<decltype(oo)>;
+      if constexpr (N <= 128) {
+        if (ht == 2)
+          hipLaunchKernelGGL((cache_attn_kernel<N, BITS, 2, T>), grid, dim3(kAttnThreads), 0, s,
+                             qq, c, a, oo);
+      }
+      if (ht == 1)
+        hipLaunchKernelGGL((cache_attn_kernel<N, BITS, 1, T>), grid, dim3(kAttnThreads), 0, s, qq,
+                           c, a, oo);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess || a.slices == 1) return e;
+      hipLaunchKernelGGL((cache_combine_kernel<N, T>), dim3(static_cast<unsigned>(B) * q_heads),
+                         dim3(kAttnThreads), 0, s, a, oo);
+      return hipGetLastError();
+    };
+    if (dt == Dt::F32) return go(static_cast<const float*>(q), static_cast<float*>(out));
+    return go(static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out));
+  });
+}
+
+}  // namespace qwha

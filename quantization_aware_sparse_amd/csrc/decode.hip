@@ -25,41 +25,23 @@
 
 #include "fwht_core.h"
 #include "launch.h"
+#include "mfma_codes.h"
 
 namespace qwha {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kDecodeWaves = 8;
 constexpr int kThreads = kDecodeWaves * 64;
 constexpr int kSpan = 128;      // columns of a span: 32 per quarter of the wave
 
-// (x & mask) | bits in one instruction, where the mask is in a vector register
-// (one scalar operand per instruction). Left to the compiler: it knows the wait
-// states between the instruction's result and a matrix instruction that reads it.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  return (x & mask) | bits;
-}
-__device__ __forceinline__ uint32_t in_vgpr(uint32_t v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-
 // Loads from a base that is the same in the whole wave plus 32-bit offsets
 // (bytes) of the lanes: one address register a lane, none per load.
 template <typename V>
 __device__ __forceinline__ V ld_at(const void* base, uint32_t off) {
   return *reinterpret_cast<const V*>(static_cast<const char*>(base) + off);
-}
-
-__device__ __forceinline__ bf16x8 as_operand(const uint32_t* d) {
-  bf16x8 r;
-  __builtin_memcpy(&r, d, 16);
-  return r;
 }
 
 // ---- codes
@@ -173,20 +155,9 @@ struct Codes {
   static __device__ __forceinline__ bf16x8 operand(const uint32_t (&u)[UW], uint32_t mask) {
     uint32_t d[4];
     if constexpr (BITS == 8) {
-      // the upper halves of fp32(q): exact, q < 2^8
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t x = u[k / 2] >> (16 * (k % 2));
-        const uint32_t lo = __float_as_uint(static_cast<float>(x & 0xFFu));
-        const uint32_t hi = __float_as_uint(static_cast<float>((x >> 8) & 0xFFu));
-        d[k] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
-      }
+      return operand8(u[0], u[1]);
     } else if constexpr (BITS == 4) {
-      // low nibbles from u << 3, high ones from u >> 1, a byte of each to a pair
-      const uint32_t lo = u[0] << 3, hi = u[0] >> 1;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        d[k] = and_or(__builtin_amdgcn_perm(hi, lo, 0x0C040C00u + 0x00010001u * k), mask, BASE);
+      return operand4(u[0], mask);
     } else if constexpr (BITS == 2) {
       const uint32_t a = u[0] << 5, b = u[0] << 3, c = u[0] << 1, e = u[0] >> 1;
 #pragma unroll
