@@ -207,30 +207,36 @@ def qwha_layer_fwd(x: torch.Tensor, codes, scales, zeros, bits: int, group: int,
 
 
 # ---------------------------------------------------------------- decoding
-def _given(dev, dtype, shape, name: str, t: torch.Tensor) -> int:
+def _given(dev: int, dtype, shape, name: str, t: torch.Tensor) -> int:
     """The address of an argument of the decoding calls, checked: a contiguous
-    tensor of this type and shape on the call's device."""
+    tensor of this type and shape on the call's device (its index; -1: the CPU)."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the call's device ({dev})")
+    raise ValueError("tensors must be contiguous")
 
 
-def _enqueue(dev, where: str, fn, *args) -> None:
+# The current stream's handle alone: torch.cuda.current_stream makes an object of
+# it, which costs half as much as a launch.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _enqueue(dev: int, where: str, fn, *args) -> None:
     """Calls fn on the current stream of the tensors' device, which need not
     be the current device."""
-    if dev.type != "cuda":
+    if dev < 0:
         raise ValueError("tensors must live on the GPU")
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(dev))
     if status != 0:
         check(status, where)
 
@@ -242,7 +248,7 @@ def qwha_layer_decode(x: torch.Tensor, codes, scales, zeros, bits: int, group: i
     z F^T for x [T][d_in], T <= QWHA_DECODE_MAX_T, bf16 or fp32 (y alike).
     Without an adapter (c None or empty) the base layer alone."""
     T, d_in = x.shape
-    dev = x.device
+    dev = x.get_device()
     d_out, groups = scales.shape
     if bits not in (2, 3, 4, 8):
         raise ValueError(f"bits={bits} is not one of 2, 3, 4, 8")
@@ -261,10 +267,11 @@ def qwha_layer_decode(x: torch.Tensor, codes, scales, zeros, bits: int, group: i
     else:
         args += (None, None, None)
     if y is None:
-        y = torch.empty((T, d_out), dtype=x.dtype, device=dev)
-    need = lib.qwha_layer_decode_workspace_bytes(T, d_in, d_out, p)
-    if ws is None and need:
-        ws = workspace(need, dev)
+        y = x.new_empty((T, d_out))
+    if ws is None:
+        need = lib.qwha_layer_decode_workspace_bytes(T, d_in, d_out, p)
+        if need:
+            ws = workspace(need, x.device)
     _enqueue(dev, "qwha_layer_decode", lib.qwha_layer_decode,
              _given(dev, x.dtype, (T, d_in), "x", x) if T else None, _dt(x), T, d_in, d_out, *args,
              float(alpha), _given(dev, x.dtype, (T, d_out), "y", y) if T else None,
@@ -300,7 +307,7 @@ def qwha_cache_write(k: torch.Tensor, v: torch.Tensor, slots, codes, scales, zer
     cache made by qwha_cache_empty; with rotate through the Walsh-Hadamard
     transform of each row."""
     T, heads, head_dim = k.shape
-    dev = k.device
+    dev = k.get_device()
     arrays, n_pages, page = _cache_args(dev, codes, scales, zeros, heads, head_dim, bits)
     _enqueue(dev, "qwha_cache_write", lib.qwha_cache_write,
              _given(dev, k.dtype, k.shape, "k", k) if T else None,
@@ -314,15 +321,15 @@ def qwha_cache_read(codes, scales, zeros, slots, bits: int, head_dim: int, rotat
                     v: Optional[torch.Tensor] = None):
     """k and v [T][heads][head_dim] of the slots (int32 [T]) of a cache; zeros
     for slots outside it."""
-    dev = codes.device
+    dev = codes.get_device()
     heads = codes.shape[2]
     T = slots.numel()
     arrays, n_pages, page = _cache_args(dev, codes, scales, zeros, heads, head_dim, bits)
     shape = (T, heads, head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=out_dtype, device=dev)
+        k = codes.new_empty(shape, dtype=out_dtype)
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=dev)
+        v = k.new_empty(shape)
     _enqueue(dev, "qwha_cache_read", lib.qwha_cache_read, *arrays, heads, head_dim, bits,
              int(rotate), n_pages, page,
              _given(dev, torch.int32, (T,), "slots", slots) if T else None, T, _dt(k),
@@ -340,15 +347,16 @@ def qwha_cache_attn(q: torch.Tensor, codes, scales, zeros, table, lens, bits: in
     table[b] (int32 [B] and [B][width]) of a cache; scale 1/sqrt(head_dim)
     unless given."""
     B, q_heads, head_dim = q.shape
-    dev = q.device
+    dev = q.get_device()
     heads = codes.shape[2]
     arrays, n_pages, page = _cache_args(dev, codes, scales, zeros, heads, head_dim, bits)
     width = table.shape[1]
     if out is None:
         out = torch.empty_like(q)
-    need = lib.qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
-    if ws is None and need:
-        ws = workspace(need, dev)
+    if ws is None:
+        need = lib.qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
+        if need:
+            ws = workspace(need, q.device)
     _enqueue(dev, "qwha_cache_attn", lib.qwha_cache_attn,
              _given(dev, q.dtype, q.shape, "q", q) if B else None, _dt(q), B, q_heads, *arrays,
              heads, head_dim, bits, int(rotate), n_pages, page,
