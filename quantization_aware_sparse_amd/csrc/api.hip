@@ -685,7 +685,7 @@ qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64
   QWHA_NEED(k, 16);
   QWHA_NEED(v, 16);
   QWHA_NEED(slots, 4);
-  const Cache c{codes, scales, zeros, n_pages, lg_page, heads, head_dim, bits};
+  const Cache c = make_cache(codes, scales, zeros, n_pages, lg_page, heads, head_dim, bits);
   return hip_check(timed(QWHA_KERNEL_CACHE_WRITE, stream,
                          [&] {
                            return launch_cache_write(k, v, static_cast<Dt>(act), T, slots, rotate,
@@ -710,8 +710,8 @@ qwha_status qwha_cache_read(const uint32_t* codes, const float* scales, const fl
   QWHA_NEED(slots, 4);
   QWHA_NEED(k, 16);
   QWHA_NEED(v, 16);
-  const Cache c{const_cast<uint32_t*>(codes), const_cast<float*>(scales),
-                const_cast<float*>(zeros), n_pages, lg_page, heads, head_dim, bits};
+  const Cache c = make_cache(const_cast<uint32_t*>(codes), const_cast<float*>(scales),
+                             const_cast<float*>(zeros), n_pages, lg_page, heads, head_dim, bits);
   return hip_check(timed(QWHA_KERNEL_CACHE_READ, stream,
                          [&] {
                            return launch_cache_read(c, slots, T, rotate,
@@ -763,8 +763,8 @@ qwha_status qwha_cache_attn(const void* q, qwha_dtype act, int32_t B, int32_t q_
       return fail(QWHA_ERR_WORKSPACE, "cache attention workspace needs %zu bytes", total);
     QWHA_NEED(workspace, 256);
   }
-  const Cache c{const_cast<uint32_t*>(codes), const_cast<float*>(scales),
-                const_cast<float*>(zeros), n_pages, lg_page, heads, head_dim, bits};
+  const Cache c = make_cache(const_cast<uint32_t*>(codes), const_cast<float*>(scales),
+                             const_cast<float*>(zeros), n_pages, lg_page, heads, head_dim, bits);
   return hip_check(timed(QWHA_KERNEL_CACHE_ATTN, stream,
                          [&] {
                            return launch_cache_attn(q, static_cast<Dt>(act), B, q_heads, c, table,

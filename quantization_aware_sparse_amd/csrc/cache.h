@@ -19,16 +19,38 @@ struct Cache {
   int lg_page;
   int heads;
   int dim, bits;
+  // x / heads = (x * heads_magic) >> heads_shift for x < 2^31, with
+  // 2^(shift - 31) the next power of two from heads on and magic =
+  // ceil(2^shift / heads): x (magic heads - 2^shift) < 2^31 heads <= 2^shift
+  uint32_t heads_magic;
+  int heads_shift;
 
+  __host__ __device__ uint32_t over_heads(uint32_t x) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(x) * heads_magic) >> heads_shift);
+  }
   // rows of one part; the offsets of a long cache pass 32 bits
   __host__ __device__ int64_t part_rows() const { return (n_pages * heads) << lg_page; }
+  // part * n_pages + page fits 32 bits (n_pages < 2^28): one 64-bit product
   __host__ __device__ int64_t row_in(int part, int32_t page, int off, int head) const {
-    return (((part * n_pages + page) * heads + head) << lg_page) + off;
+    const uint32_t g = static_cast<uint32_t>(part) * static_cast<uint32_t>(n_pages) +
+                       static_cast<uint32_t>(page);
+    return static_cast<int64_t>(((static_cast<uint64_t>(g) * static_cast<uint32_t>(heads) +
+                                  static_cast<uint32_t>(head)) << lg_page) +
+                                static_cast<uint32_t>(off));
   }
   __host__ __device__ int64_t row(int part, int32_t slot, int head) const {
     return row_in(part, slot >> lg_page, slot & ((1 << lg_page) - 1), head);
   }
 };
+
+inline Cache make_cache(uint32_t* codes, float* scales, float* zeros, int64_t n_pages, int lg_page,
+                        int heads, int dim, int bits) {
+  int s = 0;
+  while ((1 << s) < heads) ++s;
+  const uint64_t one = uint64_t{1} << (31 + s);
+  return Cache{codes, scales, zeros, n_pages, lg_page, heads, dim, bits,
+               static_cast<uint32_t>((one + heads - 1) / heads), 31 + s};
+}
 
 // Calls fn with the kernel's compile-time choices.
 template <typename Fn>

@@ -16,13 +16,14 @@ namespace qwha {
 
 namespace {
 
-template <int N, bool MAX>
+// over the LANES lanes of a row
+template <int LANES, bool MAX>
 __device__ __forceinline__ float row_extreme(float m) {
   auto pick = [](float a, float b) { return MAX ? fmaxf(a, b) : fminf(a, b); };
-  if constexpr (N > 16) m = pick(m, lane_xor<1>(m));
-  if constexpr (N > 32) m = pick(m, lane_xor<2>(m));
-  if constexpr (N > 64) m = pick(m, lane_xor<4>(m));
-  if constexpr (N > 128) m = pick(m, lane_xor<8>(m));
+  if constexpr (LANES > 1) m = pick(m, lane_xor<1>(m));
+  if constexpr (LANES > 2) m = pick(m, lane_xor<2>(m));
+  if constexpr (LANES > 4) m = pick(m, lane_xor<4>(m));
+  if constexpr (LANES > 8) m = pick(m, lane_xor<8>(m));
   return m;
 }
 
@@ -41,130 +42,199 @@ __device__ __forceinline__ float round_half_up(float v, float s, float inv) {
   return q;
 }
 
-// Written per token: keys, then values, head by head (the order of x).
-// Bound by HBM: a row reads head_dim elements and writes head_dim * b / 8 + 8
-// bytes. The transform runs in fp64: a row's sums are then exact (16-bit
-// inputs whose exponents span less than 2^37), so v, its range and every code
-// do not depend on the order of the additions.
+// Row `row` of a call's [T][2][heads] rows: keys, then values, head by head.
+struct CallRow {
+  uint32_t t;
+  int part, head;
+};
+__device__ __forceinline__ CallRow call_row(const Cache& c, uint32_t row) {
+  const uint32_t tp = c.over_heads(row);
+  return CallRow{tp >> 1, static_cast<int>(tp & 1u), static_cast<int>(row - tp * c.heads)};
+}
+
+// Bound by the vector units and then HBM: a row reads N elements and writes
+// N * b / 8 + 8 bytes. The transform runs in fp64: a row's sums are then exact
+// (16-bit inputs whose exponents span less than 2^37), so v, its range and
+// every code do not depend on the order of the additions. 32 columns a lane:
+// a stage across lanes costs 3 to 5 instructions a value (two moves, a product
+// and sum), one within a lane a single one.
+constexpr int kWritePer = 32;
+
 template <int N, int BITS, typename TIn, bool ROT>
 __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict__ k,
-                                                          const TIn* __restrict__ v, int64_t rows,
+                                                          const TIn* __restrict__ v, uint32_t rows,
                                                           const int32_t* __restrict__ slots,
                                                           Cache c) {
-  constexpr int LPR = N / 16;                  // lanes per row
+  constexpr int PER = kWritePer, LPR = N / PER;
+  constexpr int WORDS = PER * BITS / 32;
   constexpr float QMAX = static_cast<float>((1 << BITS) - 1);
   const int u = threadIdx.x % LPR;
-  // rows: [T][2][heads]
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
-  const bool live = row < rows;
-  const int64_t rr = live ? row : rows - 1;
-  const int64_t tp = rr / c.heads;
-  const int h = static_cast<int>(rr - tp * c.heads);
-  const int part = static_cast<int>(tp & 1);
-  const int64_t t = tp >> 1;
-  const int32_t slot = slots[t];
-  const bool stored = live && slot >= 0 && (slot >> c.lg_page) < c.n_pages;
+  const uint32_t row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const CallRow cr = call_row(c, min(row, rows - 1));
+  const int32_t slot = slots[cr.t];
 
-  float f[16];
+  float f[PER];
   {
-    const TIn* src = (part ? v : k) + (t * c.heads + h) * N + u * 16;
+    const TIn* src = (cr.part ? v : k) +
+                     (static_cast<uint64_t>(cr.t) * c.heads + cr.head) * N + u * PER;
     if constexpr (ROT) {
-      double a[16];
-      load16(src, a);
-      fwht_lanes<N>(a, u);
+      double a[PER];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) f[r] = static_cast<float>(a[r] * (1.0 / N));
+      for (int i = 0; i < PER / 16; ++i) load16(src + 16 * i, a + 16 * i);
+      fwht_lanes<N, PER>(a, u);
+#pragma unroll
+      for (int r = 0; r < PER; ++r) f[r] = static_cast<float>(a[r]) * (1.f / N);   // a power of two
     } else {
-      load16(src, f);
+#pragma unroll
+      for (int i = 0; i < PER / 16; ++i) load16(src + 16 * i, f + 16 * i);
     }
   }
   float lo = 0.f, hi = 0.f;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < PER; ++r) {
     lo = fminf(lo, f[r]);
     hi = fmaxf(hi, f[r]);
   }
-  lo = row_extreme<N, false>(lo);
-  hi = row_extreme<N, true>(hi);
+  lo = row_extreme<LPR, false>(lo);
+  hi = row_extreme<LPR, true>(hi);
   float s = (hi - lo) / QMAX;
   const bool flat = !(s >= 1.17549435e-38f);   // a step below fp32's normal range holds nothing
   if (flat) s = 0.f;
   const float inv = flat ? 0.f : 1.f / s;
   const float z = flat ? 0.f : round_half_up(-lo, s, inv);
-  uint32_t w[16 * BITS / 32];
+  uint32_t w[WORDS];
 #pragma unroll
-  for (int i = 0; i < 16 * BITS / 32; ++i) w[i] = 0u;
+  for (int i = 0; i < WORDS; ++i) w[i] = 0u;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const float q = flat ? 0.f : fminf(fmaxf(round_half_up(f[r], s, inv) + z, 0.f), QMAX);
+  for (int r = 0; r < PER; ++r) {
+    const float q = fminf(fmaxf(round_half_up(f[r], s, inv) + z, 0.f), QMAX);
     w[r * BITS / 32] |= static_cast<uint32_t>(q) << (r * BITS % 32);
   }
-  if (!stored) return;
-  const int64_t at = c.row(part, slot, h);
-  uint32_t* dst = c.codes + at * (N * BITS / 32) + u * (16 * BITS / 32);
-  if constexpr (BITS == 4) {
-    *reinterpret_cast<uint2*>(dst) = uint2{w[0], w[1]};
-  } else {
-    *reinterpret_cast<uint4*>(dst) = uint4{w[0], w[1], w[2], w[3]};
-  }
+  if (row >= rows || slot < 0 || (slot >> c.lg_page) >= c.n_pages) return;
+  const int64_t at = c.row(cr.part, slot, cr.head);
+  uint4* dst = reinterpret_cast<uint4*>(c.codes + at * (N * BITS / 32) + u * WORDS);
+#pragma unroll
+  for (int i = 0; i < WORDS / 4; ++i)
+    dst[i] = flat ? uint4{0u, 0u, 0u, 0u}
+                  : uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
   if (u == 0) {
     c.scales[at] = s;
     c.zeros[at] = z;
   }
 }
 
+// The transform of 16 codes a lane, two to a register of 16-bit integers:
+// sums of up to 256 codes of 4 bits, or of 8 bits less 128, fit them (for 8
+// bits and 256 columns: 128 of each sign give at most 128 * 127 + 128 * 128,
+// the row of ones at least -256 * 128), so the transform is exact and takes
+// half the instructions. z and the 128 come back in column 0, the only one in
+// which a constant row's transform is not zero.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+template <int X>
+__device__ __forceinline__ s16x2 lane_xor_s16(s16x2 v) {
+  int x;
+  __builtin_memcpy(&x, &v, 4);
+  x = lane_xor_i32<X>(x);
+  __builtin_memcpy(&v, &x, 4);
+  return v;
+}
+template <int X>
+__device__ __forceinline__ void codes_lanes(s16x2* p, int lane) {
+  const short one = lane & X ? -1 : 1;
+  const s16x2 sign = s16x2{one, one};
+#pragma unroll
+  for (int r = 0; r < 8; ++r) p[r] = p[r] * sign + lane_xor_s16<X>(p[r]);
+}
+
+// w: 16 codes (2 or 4 words) -> f[16] = their transform, less 128 times
+// N in column 0 for 8 bits
+template <int N, int BITS>
+__device__ __forceinline__ void transform_codes(const uint32_t* w, int lane, float* f) {
+  constexpr int HALF = 16 / BITS;            // codes k and k + HALF of a word share a register
+  constexpr uint32_t MASK = BITS == 4 ? 0x000F000Fu : 0x00FF00FFu;
+  s16x2 p[8];
+#pragma unroll
+  for (int i = 0; i < 16 * BITS / 32; ++i)
+#pragma unroll
+    for (int k = 0; k < HALF; ++k) {
+      const uint32_t x = (w[i] >> (BITS * k)) & MASK;
+      __builtin_memcpy(&p[i * HALF + k], &x, 4);
+      if (BITS == 8) p[i * HALF + k] -= s16x2{128, 128};
+    }
+  // register index bits (the codes' bits but the one of the halves), the
+  // halves, the lanes
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (r & h) continue;
+      const s16x2 a = p[r], b = p[r + h];
+      p[r] = a + b;
+      p[r + h] = a - b;
+    }
+#pragma unroll
+  for (int r = 0; r < 8; ++r) p[r] = p[r].yy * s16x2{1, -1} + p[r].xx;
+  if constexpr (N > 16) codes_lanes<1>(p, lane);
+  if constexpr (N > 32) codes_lanes<2>(p, lane);
+  if constexpr (N > 64) codes_lanes<4>(p, lane);
+  if constexpr (N > 128) codes_lanes<8>(p, lane);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int i = r / HALF * 2 * HALF + r % HALF;
+    f[i] = static_cast<float>(p[r].x);
+    f[i + HALF] = static_cast<float>(p[r].y);
+  }
+}
+
 // Rows [T][2][heads] of the slots, dense; a token without a slot reads as
-// zeros. Bound by HBM's writes: head_dim elements out for head_dim * b / 8 + 8
-// bytes in.
+// zeros. Bound by HBM's writes: N elements out for N * b / 8 + 8 bytes in.
 template <int N, int BITS, typename TOut, bool ROT>
 __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
                                                          const int32_t* __restrict__ slots,
-                                                         int64_t rows, TOut* __restrict__ k,
+                                                         uint32_t rows, TOut* __restrict__ k,
                                                          TOut* __restrict__ v) {
-  constexpr int LPR = N / 16;
+  constexpr int LPR = N / 16, WORDS = 16 * BITS / 32;
   const int u = threadIdx.x % LPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
-  const bool live = row < rows;
-  const int64_t rr = live ? row : rows - 1;
-  const int64_t tp = rr / c.heads;
-  const int h = static_cast<int>(rr - tp * c.heads);
-  const int part = static_cast<int>(tp & 1);
-  const int64_t t = tp >> 1;
-  const int32_t slot = slots[t];
-  float f[16];
-#pragma unroll
-  for (int r = 0; r < 16; ++r) f[r] = 0.f;
-  if (slot >= 0 && (slot >> c.lg_page) < c.n_pages) {
-    const int64_t at = c.row(part, slot, h);
-    const uint32_t* src = c.codes + at * (N * BITS / 32) + u * (16 * BITS / 32);
-    uint32_t w[16 * BITS / 32];
-    if constexpr (BITS == 4) {
-      const uint2 p = *reinterpret_cast<const uint2*>(src);
-      w[0] = p.x; w[1] = p.y;
-    } else {
-      const uint4 p = *reinterpret_cast<const uint4*>(src);
-      w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w;
-    }
-    const float s = c.scales[at], z = c.zeros[at];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const uint32_t q = (w[r * BITS / 32] >> (r * BITS % 32)) & ((1u << BITS) - 1u);
-      f[r] = (static_cast<float>(q) - z) * s;
-    }
+  const uint32_t row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const CallRow cr = call_row(c, min(row, rows - 1));
+  const int32_t slot = slots[cr.t];
+  const bool stored = slot >= 0 && (slot >> c.lg_page) < c.n_pages;
+  const int64_t at = c.row(cr.part, stored ? slot : 0, cr.head);
+  const uint32_t* src = c.codes + at * (N * BITS / 32) + u * WORDS;
+  uint32_t w[WORDS];
+  if constexpr (BITS == 4) {
+    const uint2 p = *reinterpret_cast<const uint2*>(src);
+    w[0] = p.x; w[1] = p.y;
+  } else {
+    const uint4 p = *reinterpret_cast<const uint4*>(src);
+    w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w;
   }
-  // every lane of a row takes the same branch above, so the butterflies see whole rows
-  if constexpr (ROT) fwht_lanes<N>(f, u);
-  if (live) store16((part ? v : k) + (t * c.heads + h) * N + u * 16, f);
+  const float s = c.scales[at], z = c.zeros[at];
+  float f[16];
+  if constexpr (ROT) {
+    transform_codes<N, BITS>(w, u, f);
+    if (u == 0) f[0] += static_cast<float>(N) * ((BITS == 8 ? 128.f : 0.f) - z);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      f[r] = static_cast<float>((w[r * BITS / 32] >> (r * BITS % 32)) & ((1u << BITS) - 1u)) - z;
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r) f[r] = stored ? f[r] * s : 0.f;
+  if (row < rows)
+    store16((cr.part ? v : k) + (static_cast<uint64_t>(cr.t) * c.heads + cr.head) * N + u * 16, f);
 }
 
 }  // namespace
 
 hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,
                               const int32_t* slots, int rotate, const Cache& c, hipStream_t s) {
-  const int64_t rows = T * 2 * c.heads;
+  const uint32_t rows = static_cast<uint32_t>(T * 2 * c.heads);
   return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
     constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
-    const dim3 grid(static_cast<unsigned>((rows * (N / 16) + 255) / 256));
+    constexpr int RPB = 256 / (N / kWritePer);
+    const dim3 grid((rows - 1) / RPB + 1);
     auto go = [&](auto kernel, auto* kk, auto* vv) {
       hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, kk, vv, rows, slots, c);
       return hipGetLastError();
@@ -184,10 +254,11 @@ hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,
 
 hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, int rotate, Dt dt,
                              void* k, void* v, hipStream_t s) {
-  const int64_t rows = T * 2 * c.heads;
+  const uint32_t rows = static_cast<uint32_t>(T * 2 * c.heads);
   return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
     constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
-    const dim3 grid(static_cast<unsigned>((rows * (N / 16) + 255) / 256));
+    constexpr int RPB = 256 / (N / 16);
+    const dim3 grid((rows - 1) / RPB + 1);
     auto go = [&](auto kernel, auto* kk, auto* vv) {
       hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, c, slots, rows, kk, vv);
       return hipGetLastError();

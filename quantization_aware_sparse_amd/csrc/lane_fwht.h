@@ -1,38 +1,45 @@
 // The Walsh-Hadamard transform of rows that lie across the lanes of a wave:
-// out[j] = sum_m in[m] * (-1)^popcount(m & j), N = 64, 128 or 256 columns,
-// 16 consecutive ones a lane, N / 16 neighbouring lanes a row.
+// out[j] = sum_m in[m] * (-1)^popcount(m & j), N = 64, 128 or 256 columns.
 #pragma once
 
 #include "common.h"
 
 namespace qwha {
 
-template <int X, typename Acc>
+// lane ^ X's values added, or the lane's own subtracted from them
+template <int X, int PER, typename Acc>
 __device__ __forceinline__ void butterfly_lanes(Acc* v, int lane) {
-  const bool upper = (lane & X) != 0;
+  const Acc sign = lane & X ? Acc(-1) : Acc(1);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const Acc o = lane_xor<X>(v[r]);
-    v[r] = upper ? o - v[r] : v[r] + o;
-  }
+  for (int r = 0; r < PER; ++r) v[r] = lane_xor<X>(v[r]) + sign * v[r];
 }
 
-// v H over N columns, 16 a lane
-template <int N, typename Acc>
+// v H over N columns, PER consecutive ones a lane: N / PER lanes a row
+template <int N, int PER = 16, typename Acc>
 __device__ __forceinline__ void fwht_lanes(Acc* v, int lane) {
 #pragma unroll
-  for (int h = 1; h < 16; h <<= 1)
+  for (int h = 1; h < PER; h <<= 1)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
+    for (int r = 0; r < PER; ++r) {
       if (r & h) continue;
       const Acc a = v[r], c = v[r + h];
       v[r] = a + c;
       v[r + h] = a - c;
     }
-  if constexpr (N > 16) butterfly_lanes<1>(v, lane);
-  if constexpr (N > 32) butterfly_lanes<2>(v, lane);
-  if constexpr (N > 64) butterfly_lanes<4>(v, lane);
-  if constexpr (N > 128) butterfly_lanes<8>(v, lane);
+  if constexpr (N / PER > 1) butterfly_lanes<1, PER>(v, lane);
+  if constexpr (N / PER > 2) butterfly_lanes<2, PER>(v, lane);
+  if constexpr (N / PER > 4) butterfly_lanes<4, PER>(v, lane);
+  if constexpr (N / PER > 8) butterfly_lanes<8, PER>(v, lane);
+}
+
+// two fp32 as bf16, rounded to nearest even, in one instruction
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 p = __builtin_convertvector((f32x2{lo, hi}), bf16x2);
+  uint32_t w;
+  __builtin_memcpy(&w, &p, 4);
+  return w;
 }
 
 // 16 consecutive values as fp32 or bf16 (rounded to nearest even)
@@ -45,9 +52,7 @@ __device__ __forceinline__ void store16(TOut* dst, const float* f) {
   } else {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = static_cast<uint32_t>(f32_to_bf16(f[2 * i])) |
-             (static_cast<uint32_t>(f32_to_bf16(f[2 * i + 1])) << 16);
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       reinterpret_cast<uint4*>(dst)[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
