@@ -27,19 +27,16 @@ __device__ __forceinline__ float row_extreme(float m) {
   return m;
 }
 
-// floor(v / s + 1/2) exactly, for |v| up to about 2^8 s: rint(v * (1/s)) is
-// at most one off, and the residual v - q s is exact in one fma. (Its bits:
-// where |v| >= s both v and q s are multiples of ulp(s) and the difference is
-// at most about s; below, q is 0 or +-1 and the difference is exact as one of
-// two numbers within a factor of two of each other.) So the comparison with
-// s / 2 decides the rounding as infinite precision would, and equal inputs
-// give equal codes whatever computes them.
-__device__ __forceinline__ float round_half_up(float v, float s, float inv) {
-  float q = rintf(v * inv);
-  const float r = fmaf(-q, s, v), h = 0.5f * s;
-  if (r >= h) q += 1.f;
-  if (r < -h) q -= 1.f;
-  return q;
+// floor(v / s + 1/2) + add exactly, for |v| up to about 2^8 s. The quotient
+// from the reciprocal is off by less than 2^-14, so floor(v/s + 1/2 - 2^-12) is
+// the result or, beside a border, one below it; the residual r = v - q s then
+// decides, and one fma gives it exactly: where |v| >= s both v and q s are
+// multiples of ulp(s) and r is at most s; below, q is 0 or -1 and r is v or the
+// exact difference of two numbers within a factor of two. So the code is what
+// infinite precision gives for this v and s, whatever computes it.
+__device__ __forceinline__ int round_half_up(float v, float s, float half, float inv, int add) {
+  const float q = floorf(fmaf(v, inv, 0.5f - 0x1p-12f));
+  return static_cast<int>(q) + add + (fmaf(-q, s, v) >= half ? 1 : 0);
 }
 
 // Row `row` of a call's [T][2][heads] rows: keys, then values, head by head.
@@ -100,14 +97,14 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict_
   float s = (hi - lo) / QMAX;
   const bool flat = !(s >= 1.17549435e-38f);   // a step below fp32's normal range holds nothing
   if (flat) s = 0.f;
-  const float inv = flat ? 0.f : 1.f / s;
-  const float z = flat ? 0.f : round_half_up(-lo, s, inv);
+  const float inv = flat ? 0.f : 1.f / s, half = 0.5f * s;
+  const int z = flat ? 0 : round_half_up(-lo, s, half, inv, 0);
   uint32_t w[WORDS];
 #pragma unroll
   for (int i = 0; i < WORDS; ++i) w[i] = 0u;
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
-    const float q = fminf(fmaxf(round_half_up(f[r], s, inv) + z, 0.f), QMAX);
+    const int q = min(max(round_half_up(f[r], s, half, inv, z), 0), (1 << BITS) - 1);
     w[r * BITS / 32] |= static_cast<uint32_t>(q) << (r * BITS % 32);
   }
   if (row >= rows || slot < 0 || (slot >> c.lg_page) >= c.n_pages) return;
@@ -119,7 +116,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict_
                   : uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
   if (u == 0) {
     c.scales[at] = s;
-    c.zeros[at] = z;
+    c.zeros[at] = static_cast<float>(z);
   }
 }
 
@@ -189,6 +186,9 @@ __device__ __forceinline__ void transform_codes(const uint32_t* w, int lane, flo
 
 // Rows [T][2][heads] of the slots, dense; a token without a slot reads as
 // zeros. Bound by HBM's writes: N elements out for N * b / 8 + 8 bytes in.
+// Lane u of a row holds the columns 8u .. + 8 of either half of the row (the
+// transform takes the index bits in any order), so that a store instruction
+// covers whole lines of bf16.
 template <int N, int BITS, typename TOut, bool ROT>
 __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
                                                          const int32_t* __restrict__ slots,
@@ -201,14 +201,16 @@ __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
   const int32_t slot = slots[cr.t];
   const bool stored = slot >= 0 && (slot >> c.lg_page) < c.n_pages;
   const int64_t at = c.row(cr.part, stored ? slot : 0, cr.head);
-  const uint32_t* src = c.codes + at * (N * BITS / 32) + u * WORDS;
+  const uint32_t* src = c.codes + at * (N * BITS / 32) + u * (WORDS / 2);
   uint32_t w[WORDS];
-  if constexpr (BITS == 4) {
-    const uint2 p = *reinterpret_cast<const uint2*>(src);
-    w[0] = p.x; w[1] = p.y;
-  } else {
-    const uint4 p = *reinterpret_cast<const uint4*>(src);
-    w[0] = p.x; w[1] = p.y; w[2] = p.z; w[3] = p.w;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (BITS == 4) {
+      w[i] = src[i * LPR];
+    } else {
+      const uint2 p = reinterpret_cast<const uint2*>(src)[i * LPR];
+      w[2 * i] = p.x; w[2 * i + 1] = p.y;
+    }
   }
   const float s = c.scales[at], z = c.zeros[at];
   float f[16];
@@ -222,8 +224,10 @@ __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
   }
 #pragma unroll
   for (int r = 0; r < 16; ++r) f[r] = stored ? f[r] * s : 0.f;
-  if (row < rows)
-    store16((cr.part ? v : k) + (static_cast<uint64_t>(cr.t) * c.heads + cr.head) * N + u * 16, f);
+  if (row >= rows) return;
+  TOut* dst = (cr.part ? v : k) + (static_cast<uint64_t>(cr.t) * c.heads + cr.head) * N + u * 8;
+  store8(dst, f);
+  store8(dst + N / 2, f + 8);
 }
 
 }  // namespace

@@ -42,21 +42,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return w;
 }
 
-// 16 consecutive values as fp32 or bf16 (rounded to nearest even)
+// 8 or 16 consecutive values as fp32 or bf16 (rounded to nearest even)
 template <typename TOut>
-__device__ __forceinline__ void store16(TOut* dst, const float* f) {
+__device__ __forceinline__ void store8(TOut* dst, const float* f) {
   if constexpr (sizeof(TOut) == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
       reinterpret_cast<float4*>(dst)[i] = float4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
   } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      reinterpret_cast<uint4*>(dst)[i] = uint4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    *reinterpret_cast<uint4*>(dst) = uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
   }
+}
+template <typename TOut>
+__device__ __forceinline__ void store16(TOut* dst, const float* f) {
+  store8(dst, f);
+  store8(dst + 8, f + 8);
 }
 
 }  // namespace qwha
