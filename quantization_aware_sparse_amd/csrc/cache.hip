@@ -189,46 +189,66 @@ __device__ __forceinline__ void transform_codes(const uint32_t* w, int lane, flo
 // Lane u of a row holds the columns 8u .. + 8 of either half of the row (the
 // transform takes the index bits in any order), so that a store instruction
 // covers whole lines of bf16.
-template <int N, int BITS, typename TOut, bool ROT>
+// IT rows a lane, their loads in flight together. Calls of many rows take 4 and
+// store past the caches, whose lines the codes then keep: 40000 tokens of 8
+// heads of 128 (209 MB) 49.1 us with one row and plain stores, 46.6 with 4 rows,
+// 34.8 with stores past the caches too.
+template <int N, int BITS, typename TOut, bool ROT, int IT>
 __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
                                                          const int32_t* __restrict__ slots,
                                                          uint32_t rows, TOut* __restrict__ k,
                                                          TOut* __restrict__ v) {
-  constexpr int LPR = N / 16, WORDS = 16 * BITS / 32;
+  constexpr int LPR = N / 16, RPB = 256 / LPR, WORDS = 16 * BITS / 32;
   const int u = threadIdx.x % LPR;
-  const uint32_t row = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  const CallRow cr = call_row(c, min(row, rows - 1));
-  const int32_t slot = slots[cr.t];
-  const bool stored = slot >= 0 && (slot >> c.lg_page) < c.n_pages;
-  const int64_t at = c.row(cr.part, stored ? slot : 0, cr.head);
-  const uint32_t* src = c.codes + at * (N * BITS / 32) + u * (WORDS / 2);
-  uint32_t w[WORDS];
+  const uint32_t row0 = blockIdx.x * (RPB * IT) + threadIdx.x / LPR;
+  uint32_t w[IT][WORDS];
+  float s[IT], z[IT];
+  CallRow cr[IT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (BITS == 4) {
-      w[i] = src[i * LPR];
+  for (int j = 0; j < IT; ++j) {
+    cr[j] = call_row(c, min(row0 + j * RPB, rows - 1));
+    const int32_t slot = slots[cr[j].t];
+    const bool stored = slot >= 0 && (slot >> c.lg_page) < c.n_pages;
+    const int64_t at = c.row(cr[j].part, stored ? slot : 0, cr[j].head);
+    const uint32_t* src = c.codes + at * (N * BITS / 32) + u * (WORDS / 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (BITS == 4) {
+        w[j][i] = src[i * LPR];
+      } else {
+        const uint2 p = reinterpret_cast<const uint2*>(src)[i * LPR];
+        w[j][2 * i] = p.x; w[j][2 * i + 1] = p.y;
+      }
+    }
+    // a token without a slot: 0 times whatever finite codes slot 0 holds
+    const float sv = c.scales[at], zv = c.zeros[at];
+    s[j] = stored ? sv : 0.f;
+    z[j] = stored ? zv : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < IT; ++j) {
+    float f[16];
+    if constexpr (ROT) {
+      transform_codes<N, BITS>(w[j], u, f);
+      if (u == 0) f[0] += static_cast<float>(N) * ((BITS == 8 ? 128.f : 0.f) - z[j]);
     } else {
-      const uint2 p = reinterpret_cast<const uint2*>(src)[i * LPR];
-      w[2 * i] = p.x; w[2 * i + 1] = p.y;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        f[r] = static_cast<float>((w[j][r * BITS / 32] >> (r * BITS % 32)) & ((1u << BITS) - 1u)) - z[j];
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) f[r] *= s[j];
+    if (row0 + j * RPB < rows) {
+      TOut* dst = (cr[j].part ? v : k) +
+                  (static_cast<uint64_t>(cr[j].t) * c.heads + cr[j].head) * N + u * 8;
+      store8<IT == 4>(dst, f);
+      store8<IT == 4>(dst + N / 2, f + 8);
     }
   }
-  const float s = c.scales[at], z = c.zeros[at];
-  float f[16];
-  if constexpr (ROT) {
-    transform_codes<N, BITS>(w, u, f);
-    if (u == 0) f[0] += static_cast<float>(N) * ((BITS == 8 ? 128.f : 0.f) - z);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      f[r] = static_cast<float>((w[r * BITS / 32] >> (r * BITS % 32)) & ((1u << BITS) - 1u)) - z;
-  }
-#pragma unroll
-  for (int r = 0; r < 16; ++r) f[r] = stored ? f[r] * s : 0.f;
-  if (row >= rows) return;
-  TOut* dst = (cr.part ? v : k) + (static_cast<uint64_t>(cr.t) * c.heads + cr.head) * N + u * 8;
-  store8(dst, f);
-  store8(dst + N / 2, f + 8);
 }
+
+// More rows than this (32 MB of fp32 at 128 columns) are streamed, 4 a lane.
+constexpr uint32_t kManyRows = 65536;
 
 }  // namespace
 
@@ -260,23 +280,23 @@ hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, in
                              void* k, void* v, hipStream_t s) {
   const uint32_t rows = static_cast<uint32_t>(T * 2 * c.heads);
   return by_shape(c.dim, c.bits, [&](auto n, auto bits) {
-    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
-    constexpr int RPB = 256 / (N / 16);
-    const dim3 grid((rows - 1) / RPB + 1);
-    auto go = [&](auto kernel, auto* kk, auto* vv) {
-      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, c, slots, rows, kk, vv);
+    constexpr int N = decltype(n)::value, BITS = decltype(bits)::value, RPB = 256 / (N / 16);
+    auto go = [&](auto it, auto rot, auto* kk, auto* vv) {
+      using T = std::remove_pointer_t<decltype(kk)>;
+      constexpr int IT = decltype(it)::value;
+      hipLaunchKernelGGL((cache_read_kernel<N, BITS, T, decltype(rot)::value, IT>),
+                         dim3((rows - 1) / (RPB * IT) + 1), dim3(256), 0, s, c, slots, rows, kk, vv);
       return hipGetLastError();
     };
-    if (dt == Dt::F32) {
-      auto* kk = static_cast<float*>(k);
-      auto* vv = static_cast<float*>(v);
-      return rotate ? go(cache_read_kernel<N, BITS, float, true>, kk, vv)
-                    : go(cache_read_kernel<N, BITS, float, false>, kk, vv);
-    }
-    auto* kk = static_cast<uint16_t*>(k);
-    auto* vv = static_cast<uint16_t*>(v);
-    return rotate ? go(cache_read_kernel<N, BITS, uint16_t, true>, kk, vv)
-                  : go(cache_read_kernel<N, BITS, uint16_t, false>, kk, vv);
+    auto by_rows = [&](auto rot, auto* kk, auto* vv) {
+      return rows > kManyRows ? go(std::integral_constant<int, 4>{}, rot, kk, vv)
+                              : go(std::integral_constant<int, 1>{}, rot, kk, vv);
+    };
+    auto by_type = [&](auto rot) {
+      if (dt == Dt::F32) return by_rows(rot, static_cast<float*>(k), static_cast<float*>(v));
+      return by_rows(rot, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
+    };
+    return rotate ? by_type(std::true_type{}) : by_type(std::false_type{});
   });
 }
 

@@ -42,16 +42,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return w;
 }
 
-// 8 or 16 consecutive values as fp32 or bf16 (rounded to nearest even)
-template <typename TOut>
+// 8 or 16 consecutive values as fp32 or bf16 (rounded to nearest even); STREAM:
+// past the caches, for outputs larger than they are
+template <bool STREAM = false, typename TOut>
 __device__ __forceinline__ void store8(TOut* dst, const float* f) {
+  typedef float f32x4v __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
   if constexpr (sizeof(TOut) == 4) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      reinterpret_cast<float4*>(dst)[i] = float4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+    for (int i = 0; i < 2; ++i) {
+      f32x4v* p = reinterpret_cast<f32x4v*>(dst) + i;
+      const f32x4v x = f32x4v{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+      if constexpr (STREAM) __builtin_nontemporal_store(x, p); else *p = x;
+    }
   } else {
-    *reinterpret_cast<uint4*>(dst) = uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+    u32x4v* p = reinterpret_cast<u32x4v*>(dst);
+    const u32x4v x = u32x4v{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                            pack_bf16(f[6], f[7])};
+    if constexpr (STREAM) __builtin_nontemporal_store(x, p); else *p = x;
   }
 }
 template <typename TOut>
