@@ -4,13 +4,15 @@
 //
 //   decode_kernel       up to 16 bf16 or 4 fp32 tokens: the base product on the
 //                       bf16 matrix cores, the codes read once, K split over
-//                       the waves of a workgroup, and the nonzeros of the same
-//                       rows of F;
+//                       the waves of a workgroup; with few tokens also the
+//                       nonzeros of the same rows of F, the tokens transformed
+//                       by every workgroup for itself;
 //   decode_wide_kernel  more tokens: K split over workgroups, partial sums;
-//   decode_finish_kernel  the partial sums and the nonzeros of F added up;
-//   decode_z_kernel     z, transposed: zt[column][token], so that one nonzero
-//                       of F finds its column's tokens side by side (left out
-//                       where decode_kernel transforms the tokens itself).
+//   decode_finish_kernel  partial sums and the nonzeros of F added up.
+// Where z goes through memory, the first workgroups of the product's launch
+// write it, transposed (zt[column][token], so that one nonzero of F finds its
+// column's tokens side by side): the product does not need it, the finishing
+// pass does.
 //
 // The base product per group g of columns, with codes q and OFF = 2^bits:
 //   sum_j x_j (q_j - z) s = s (sum_j x_j (OFF + q_j) - (OFF + z) sum_j x_j).
@@ -248,8 +250,31 @@ struct DecodeArgs {
   const float* c;
   float alpha;                 // alpha / b for the plain sums of a transform in LDS
   int log_b;
-  float* part;                 // decode_wide_kernel: [slices][tokens][N]
+  float* part;                 // partial sums [slices][tokens][N], where a finishing pass follows
   int slices;
+  float* z_out;                // zt, written by the launch's first z_blocks workgroups
+  int z_cols, z_blocks;        // columns of a token that one of them transforms
+};
+
+// Steps and zeros of a span's groups for one row: G neighbours in memory.
+template <int G>
+struct Groups {
+  float v[G];
+  // `row`: the tile's first row, `off` the lane's row in bytes, `g` the span's
+  // first group; where the row has fewer than G left, its last one repeats
+  __device__ __forceinline__ void load(const float* row, uint32_t off, int g, int gpr) {
+    if constexpr (G == 1) {
+      v[0] = ld_at<float>(row + g, off);
+    } else if (g + G <= gpr) {
+      typedef float any __attribute__((ext_vector_type(G), aligned(4)));
+      const any x = ld_at<any>(row + g, off);
+#pragma unroll
+      for (int i = 0; i < G; ++i) v[i] = x[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; ++i) v[i] = ld_at<float>(row + min(g + i, gpr - 1), off);
+    }
+  }
 };
 
 // The product of one span: acc += s (x (OFF + q) - (OFF + z) sum x), group by
@@ -257,8 +282,8 @@ struct DecodeArgs {
 // 4 (l / 16) .. + 4 of tile i.
 template <int BITS, int MODE, int MT, int NT>
 __device__ __forceinline__ void span_product(const uint32_t* tiles, const Codes<BITS> (&cw)[NT],
-                                             const float (&sc)[NT][1 << MODE],
-                                             const float (&zo)[NT][1 << MODE], bool half_span,
+                                             const Groups<1 << MODE> (&sc)[NT],
+                                             const Groups<1 << MODE> (&zo)[NT], bool half_span,
                                              uint32_t mask, bf16x8 ones, int lr, int lq,
                                              f32x4 (&acc)[MT][NT]) {
   using Code = Codes<BITS>;
@@ -288,12 +313,12 @@ __device__ __forceinline__ void span_product(const uint32_t* tiles, const Codes<
     if (s % PER == PER - 1) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const float z = Code::OFF + zo[j][s / PER];
+        const float z = Code::OFF + zo[j].v[s / PER];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[i][j][r] = fmaf(sc[j][s / PER], fmaf(-z, xs[i][r], g[i][j][r]), acc[i][j][r]);
+            acc[i][j][r] = fmaf(sc[j].v[s / PER], fmaf(-z, xs[i][r], g[i][j][r]), acc[i][j][r]);
       }
     }
   }
@@ -357,7 +382,7 @@ __device__ __forceinline__ void butterflies(float* v, int b) {
 // z[t * zld + zpad(column)] <- x H per block of 2^log_b columns, unscaled:
 // passes of 4 index bits, 16 values a thread, in place. `raw` holds the
 // thread's first 16 values (fetched before anything else is waited for).
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ void local_transform(const T* __restrict__ x, Raw16<T> raw, int items,
                                                 int per, int log_b, int zld, float* z) {
   float v[16];
@@ -365,7 +390,7 @@ __device__ __forceinline__ void local_transform(const T* __restrict__ x, Raw16<T
   for (int e = threadIdx.x; e < items;) {
     raw.get(v);
     const int t = e / per, u = e - t * per;
-    e += kThreads;
+    e += THREADS;
     if (e < items) raw.load(x + static_cast<int64_t>(e) * 16);
 #pragma unroll
     for (int b = 0; b < 4; ++b) butterflies(v, b);
@@ -378,7 +403,7 @@ __device__ __forceinline__ void local_transform(const T* __restrict__ x, Raw16<T
   for (int done = 4; done < log_b; done += 4) {
     const int lo = min(done, log_b - 4);
 #pragma unroll 1
-    for (int e = threadIdx.x; e < items; e += kThreads) {
+    for (int e = threadIdx.x; e < items; e += THREADS) {
       const int t = e / per, u = e - t * per;
       float* zr = z + t * zld;
       const int j0 = (u & ((1 << lo) - 1)) | ((u >> lo) << (lo + 4));
@@ -394,25 +419,28 @@ __device__ __forceinline__ void local_transform(const T* __restrict__ x, Raw16<T
   }
 }
 
-// zt[column][tp] of one token per workgroup
-template <typename T>
-__global__ __launch_bounds__(kThreads) void decode_z_kernel(const T* __restrict__ x, int K,
-                                                            int log_b, int tp,
-                                                            float* __restrict__ zt) {
-  extern __shared__ float zl[];
-  const T* row = x + static_cast<int64_t>(blockIdx.x) * K;
-  const int items = K >> 4;
+// zt[column][token] for z_cols columns (whole blocks) of one token: workgroup
+// `block` of the launch.
+template <int THREADS, typename T>
+__device__ __forceinline__ void write_z(const T* __restrict__ x, const DecodeArgs& a, int block,
+                                        float* lds) {
+  const int per = (a.K + a.z_cols - 1) / a.z_cols;
+  const int t = block / per, c0 = block % per * a.z_cols;
+  const int cols = min(a.z_cols, a.K - c0), items = cols >> 4;
+  const T* row = x + static_cast<int64_t>(t) * a.K + c0;
   Raw16<T> raw;
   raw.load(row + 16 * min(static_cast<int>(threadIdx.x), items - 1));
-  local_transform(row, raw, items, items, log_b, zpad(K), zl);
-  const float scale = 1.f / static_cast<float>(1 << log_b);
-  for (int j = threadIdx.x; j < K; j += kThreads)
-    zt[static_cast<int64_t>(j) * tp + blockIdx.x] = zl[zpad(j)] * scale;
+  local_transform<THREADS>(row, raw, items, items, a.log_b, zpad(cols), lds);
+  const float scale = 1.f / static_cast<float>(1 << a.log_b);
+  float* out = a.z_out + static_cast<int64_t>(c0) * a.tp + t;
+  for (int j = threadIdx.x; j < cols; j += THREADS)
+    out[static_cast<int64_t>(j) * a.tp] = lds[zpad(j)] * scale;
 }
 
-// ---- the nonzeros of 16 NT rows of F: side by side in E and c. The first
-// kEntries of them are fetched beside the codes and wait in LDS, so that only
-// the gather of z is left behind the product. 64 / RPW lanes take a row.
+// ---- the nonzeros of some rows of F: side by side in E and c. The first
+// kEntries of them are fetched beside whatever comes first and wait in LDS, so
+// that only the gather of z is left; each further round's are fetched while the
+// one before is worked on. 64 / RPW lanes take a row.
 constexpr int kEntries = 4 * kThreads;
 constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
 constexpr int kLocalTokens = 4;
@@ -420,7 +448,7 @@ constexpr int kLocalTokens = 4;
 struct Entries {
   uint2 e[4];                            // column, value
   __device__ __forceinline__ void load(const DecodeArgs& a, int kb, int kend) {
-    if (kend == kb) return;
+    if (kend <= kb) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t at =
@@ -434,8 +462,8 @@ struct Entries {
   }
 };
 
-// Sums over the lanes that differ in the bits from `from` to 64 / RPW (a
-// power of two each): within rows of 16 lanes through DPP.
+// Sums over the LANES lanes of a row that hold the same tokens: those that
+// differ in the bits from `from` on. Within rows of 16 lanes through DPP.
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v, int from) {
   if (from <= 1) v += lane_xor<1>(v);
@@ -445,22 +473,24 @@ __device__ __forceinline__ float lanes_sum(float v, int from) {
   if constexpr (LANES > 16) {
     if (from <= 16) v += __shfl_xor(v, 16);
   }
+  if constexpr (LANES > 32) {
+    if (from <= 32) v += __shfl_xor(v, 32);
+  }
   return v;
 }
 
-// ad[row][token] for the workgroup's 8 RPW rows and its tokens t0 ..; entries
-// beyond the staged ones follow in further rounds. LOCAL: z in LDS, a lane a
-// nonzero, its tokens one after the other; else min(tp, TB) / 4 lanes hold 4
-// tokens each of a nonzero's column. All threads call it.
+// ad[row][token] for the workgroup's 8 RPW rows. LOCAL: z in LDS, a lane a
+// nonzero, its tokens one after the other; else lpn lanes hold 4 tokens each of
+// a nonzero's column. All threads call it.
 template <int RPW, bool LOCAL, int LDA>
 __device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2* ent, int k0,
-                                         int kend, int beg, int end, int t0, int lpn,
-                                         const float* zl, float (*ad)[LDA]) {
+                                         int kend, int beg, int end, int lpn, const float* zl,
+                                         float (*ad)[LDA]) {
   constexpr int LPR = 64 / RPW;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int in_row = lane & (LPR - 1);
   const int npw = LPR / lpn, sub = in_row / lpn;
-  const float* zg = a.zt + t0 + (in_row & (lpn - 1)) * 4;
+  const float* zg = a.zt + (in_row & (lpn - 1)) * 4;
   const int zld = zpad(a.K);
   f32x4 s4 = f32x4{0.f, 0.f, 0.f, 0.f};
   int kb = k0;
@@ -470,7 +500,8 @@ __device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2
     __syncthreads();
     const int held = min(kend - kb, kEntries);
     const int e1 = min(end - kb, held);
-#pragma unroll 4
+    if (held < kend - kb) en.load(a, kb + held, kend);
+#pragma clang loop unroll_count(LOCAL ? 2 : 8)
     for (int k = max(beg - kb, 0) + sub; k < e1; k += npw) {
       const uint2 e = ent[k];
       const float cv = __uint_as_float(e.y);
@@ -491,7 +522,6 @@ __device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2
     if (held == kend - kb) break;
     kb += held;
     __syncthreads();
-    en.load(a, kb, kend);
   }
   s4[0] = lanes_sum<LPR>(s4[0], lpn);
   if (a.tokens > 1)
@@ -504,43 +534,50 @@ __device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2
 
 // ---- up to 16 bf16 or 4 fp32 tokens
 // A workgroup takes 16 NT rows of W; its waves take the spans in turn, D of
-// them on their way at any time, and add up their sums in LDS. With few tokens
-// every workgroup transforms them itself while its codes are on their way
-// (LOCAL): one launch, and no way through memory for z. The code is kept short
-// (loops, no peeled copies): a workgroup runs through much of it once, and
+// them on their way at any time, and add up their sums in LDS. The code is kept
+// short (loops, no peeled copies): a workgroup runs through much of it once, and
 // fetching instructions costs as much as fetching codes. FEW: at most 4 tokens,
 // of whose tiles only the first 4 rows are staged (the others' results are not
-// used, whatever they hold).
+// used, whatever they hold). LOCAL: every workgroup transforms the tokens for
+// itself while its codes are on their way, and adds its rows of F: one launch,
+// and no way through memory for z.
+// With groups of 128 and more the rows' steps and zeros, one run of memory, are
+// staged in LDS: read span by span they cost twice the codes' instructions, and
+// it is the rate of such scattered reads that bounds the kernel.
 template <int BITS, int MODE, int NT, typename T, bool FEW, bool LOCAL>
 __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ x, DecodeArgs a,
                                                           T* __restrict__ y) {
   constexpr int TB = Rows<T>::TOK;
   constexpr int D = 4;                               // spans on their way
   constexpr int G = 1 << MODE;
+  constexpr bool STAGED = MODE == kWide;             // steps and zeros in LDS
   constexpr int PX = sizeof(T) == 2 && !FEW ? 4 : 1; // pieces of a span per lane
   constexpr int RPW = 2 * NT;                        // rows of F per wave
   constexpr int LD = 16 * NT + 1;
   using Code = Codes<BITS>;
   __shared__ __attribute__((aligned(16))) uint32_t own[kDecodeWaves][kTileWords];
-  __shared__ float ad[16 * NT][TB + 4];
-  __shared__ uint2 ent[kEntries];
-  extern __shared__ float zl[];                      // LOCAL: [tokens][zpad(K)]
+  __shared__ float ad[LOCAL ? 16 * NT : 1][LOCAL ? 8 : 1];
+  __shared__ uint2 ent[LOCAL ? kEntries : 1];
+  extern __shared__ __attribute__((aligned(16))) float dyn[];   // steps and zeros, then z
+  if (static_cast<int>(blockIdx.x) < a.z_blocks) {
+    write_z<kThreads>(x, a, blockIdx.x, dyn);
+    return;
+  }
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NT;
+  const int n0 = (blockIdx.x - a.z_blocks) * 16 * NT;
   const int spans = (a.K + kSpan - 1) / kSpan;
-  const bool adapter = a.row_ptr != nullptr;
+  const int rows = min(16 * NT, a.N - n0);
 
   int k0 = 0, kend = 0, beg = 0, end = 0;
   Raw16<T> raw;
-  if (adapter) {
+  if constexpr (LOCAL) {
     k0 = a.row_ptr[n0];
-    kend = a.row_ptr[min(n0 + 16 * NT, a.N)];
+    kend = a.row_ptr[n0 + rows];
     const int row = n0 + w * RPW + lane / (64 / RPW);
     beg = a.row_ptr[min(row, a.N)];
     end = a.row_ptr[min(row + 1, a.N)];
-    if constexpr (LOCAL)
-      raw.load(x + 16 * min(static_cast<int>(threadIdx.x), (a.tokens * a.K >> 4) - 1));
+    raw.load(x + 16 * min(static_cast<int>(threadIdx.x), (a.tokens * a.K >> 4) - 1));
   }
   const uint32_t* ctile = a.qw.codes + static_cast<int64_t>(n0) * a.qw.wpr;
   const float* stile = a.qw.scales + static_cast<int64_t>(n0) * a.qw.gpr;
@@ -548,9 +585,9 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
   uint32_t coff[NT], soff[NT], xoff[PX];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int n = min(j * 16 + lr, a.N - 1 - n0);       // rows past N repeat the last
+    const int n = min(j * 16 + lr, rows - 1);           // rows past N repeat the last
     coff[j] = 4u * n * a.qw.wpr;
-    soff[j] = 4u * n * a.qw.gpr;
+    soff[j] = STAGED ? n * (a.qw.gpr + 1) : 4u * n * a.qw.gpr;
   }
 #pragma unroll
   for (int i = 0; i < PX; ++i)                          // tokens past the last repeat it
@@ -558,7 +595,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
 
   struct Slot {
     Code cw[NT];
-    float sc[NT][G], zo[NT][G];
+    Groups<G> sc[NT], zo[NT];
     Piece<T> xp[PX];
   } slot[D];
   auto fetch = [&](Slot& s, int span) {
@@ -566,11 +603,9 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       s.cw[j].load(ctile, coff[j], min(c0 + 32 * lq, a.K - 32));
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int gi = MODE == kWide ? c0 >> a.qw.lg_group : min((c0 >> a.qw.lg_group) + g, a.qw.gpr - 1);
-        s.sc[j][g] = ld_at<float>(stile + gi, soff[j]);
-        s.zo[j][g] = ld_at<float>(ztile + gi, soff[j]);
+      if constexpr (!STAGED) {
+        s.sc[j].load(stile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
+        s.zo[j].load(ztile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
       }
     }
 #pragma unroll
@@ -578,11 +613,24 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(slot[d], w + d * kDecodeWaves);
+  // rows of gpr steps, padded by one, and as many zeros
+  float* steps = dyn;
+  float* zeros = dyn + 16 * NT * (a.qw.gpr + 1);
+  if constexpr (STAGED) {
+#pragma unroll 1
+    for (int r = w; r < rows; r += kDecodeWaves)
+      for (int g = lane; g < a.qw.gpr; g += 64) {
+        steps[r * (a.qw.gpr + 1) + g] = stile[r * a.qw.gpr + g];
+        zeros[r * (a.qw.gpr + 1) + g] = ztile[r * a.qw.gpr + g];
+      }
+  }
+  float* zl = dyn + (STAGED ? 32 * NT * (a.qw.gpr + 1) : 0);   // LOCAL: [tokens][zpad(K)]
   Entries en;
-  if (adapter) {
+  if constexpr (LOCAL) {
     en.load(a, k0, kend);
-    if constexpr (LOCAL)
-      local_transform(x, raw, a.tokens * a.K >> 4, a.K >> 4, a.log_b, zpad(a.K), zl);
+    local_transform<kThreads>(x, raw, a.tokens * a.K >> 4, a.K >> 4, a.log_b, zpad(a.K), zl);
+  } else if constexpr (STAGED) {
+    __syncthreads();
   }
 
   const uint32_t mask = in_vgpr(Code::MASK);
@@ -596,6 +644,14 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
     for (int d = 0; d < D; ++d) {
       const int span = s0 + d * kDecodeWaves;
       if (span >= spans) break;
+      if constexpr (STAGED) {
+        const int g = span * kSpan >> a.qw.lg_group;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          slot[d].sc[j].v[0] = steps[soff[j] + g];
+          slot[d].zo[j].v[0] = zeros[soff[j] + g];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < PX; ++i) slot[d].xp[i].store(own[w], 4 * i + lq, lr);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -615,24 +671,29 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
       red[lq * LD + j * 16 + lr] = acc[0][j][0] + acc[0][j][1] + acc[0][j][2];
     }
   }
-  if (adapter)
-    nonzeros<RPW, LOCAL>(a, en, ent, k0, kend, beg, end, 0, LOCAL ? 1 : min(a.tp, TB) / 4, zl, ad);
+  if constexpr (LOCAL) nonzeros<RPW, true>(a, en, ent, k0, kend, beg, end, 1, zl, ad);
   __syncthreads();
   for (int e = threadIdx.x; e < a.tokens * 16 * NT; e += kThreads) {
     const int t = e / (16 * NT), n = e % (16 * NT);
-    if (n0 + n >= a.N) continue;
+    if (n >= rows) continue;
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) v += __uint_as_float(own[i][t * LD + n]);
-    if (adapter) v = fmaf(a.alpha, ad[n][t], v);
-    Elem<T>::st(y, static_cast<int64_t>(t) * a.N + n0 + n, v);
+    const int64_t at = static_cast<int64_t>(t) * a.N + n0 + n;
+    if (!LOCAL && a.part != nullptr) {
+      a.part[at] = v;
+    } else {
+      if constexpr (LOCAL) v = fmaf(a.alpha, ad[n][t], v);
+      Elem<T>::st(y, at, v);
+    }
   }
 }
 
 // ---- more tokens: 64 rows of tokens (64 bf16 or 16 fp32 ones) by 128 rows of W
 // per workgroup, a wave 32 of them; the tokens' tiles are staged once for all
 // waves, and the spans are split over `slices` workgroups, whose partial sums
-// decode_finish_kernel adds up.
+// decode_finish_kernel adds up. Two spans are on their way while a third is
+// worked on: with one the kernel waits for memory at every span.
 constexpr int kWideThreads = 256;
 constexpr int kWideRows = 128;
 constexpr int kWideTiles = 4;
@@ -640,17 +701,27 @@ constexpr int kWideTiles = 4;
 template <int BITS, int MODE, typename T>
 __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* __restrict__ x,
                                                                       DecodeArgs a) {
-  constexpr int MT = kWideTiles, NT = 2, G = 1 << MODE;
+  constexpr int MT = kWideTiles, NT = 2, G = 1 << MODE, D = 3;
   constexpr int TB = Rows<T>::TOK * MT;
   constexpr int PX = TB * 16 / kWideThreads;           // pieces of a span per thread
   using Code = Codes<BITS>;
-  __shared__ __attribute__((aligned(16))) uint32_t tiles[2][MT * kTileWords];
+  extern __shared__ __attribute__((aligned(16))) float dyn[];
+  if (static_cast<int>(blockIdx.x) < a.z_blocks) {
+    write_z<kWideThreads>(x, a, blockIdx.x, dyn);
+    return;
+  }
+  uint32_t* tiles = reinterpret_cast<uint32_t*>(dyn);  // two buffers
+  const int tiles_n = (a.N + kWideRows - 1) / kWideRows;
+  int block = blockIdx.x - a.z_blocks;
+  const int bn = block % tiles_n;
+  block /= tiles_n;
+  const int slice = block % a.slices, bt = block / a.slices;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * kWideRows + w * 32, t0 = blockIdx.y * TB;
+  const int n0 = bn * kWideRows + w * 32, t0 = bt * TB;
   const int spans = (a.K + kSpan - 1) / kSpan;
-  const int first = static_cast<int>(static_cast<int64_t>(spans) * blockIdx.z / a.slices);
-  const int last = static_cast<int>(static_cast<int64_t>(spans) * (blockIdx.z + 1) / a.slices);
+  const int first = static_cast<int>(static_cast<int64_t>(spans) * slice / a.slices);
+  const int last = static_cast<int>(static_cast<int64_t>(spans) * (slice + 1) / a.slices);
 
   const int nb = min(n0, a.N - 1);                      // waves past N repeat the last row
   const uint32_t* ctile = a.qw.codes + static_cast<int64_t>(nb) * a.qw.wpr;
@@ -670,22 +741,18 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
 
   struct Slot {
     Code cw[NT];
-    float sc[NT][G], zo[NT][G];
-  } slot[2];
-  Piece<T> xp[PX];
+    Groups<G> sc[NT], zo[NT];
+    Piece<T> xp[PX];
+  } slot[D];
   auto fetch = [&](Slot& s, int span) {
     const int c0 = span * kSpan;
 #pragma unroll
-    for (int i = 0; i < PX; ++i) xp[i].load(x, xoff[i], min(c0 + 8 * piece, a.K - 8));
+    for (int i = 0; i < PX; ++i) s.xp[i].load(x, xoff[i], min(c0 + 8 * piece, a.K - 8));
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       s.cw[j].load(ctile, coff[j], min(c0 + 32 * lq, a.K - 32));
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int gi = MODE == kWide ? c0 >> a.qw.lg_group : min((c0 >> a.qw.lg_group) + g, a.qw.gpr - 1);
-        s.sc[j][g] = ld_at<float>(stile + gi, soff[j]);
-        s.zo[j][g] = ld_at<float>(ztile + gi, soff[j]);
-      }
+      s.sc[j].load(stile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
+      s.zo[j].load(ztile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
     }
   };
   const uint32_t mask = in_vgpr(Code::MASK);
@@ -695,29 +762,34 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (first < last) fetch(slot[0], first);
-#pragma unroll 1
-  for (int s0 = first; s0 < last; s0 += 2) {
 #pragma unroll
-    for (int d = 0; d < 2; ++d) {
+  for (int d = 0; d < D - 1; ++d)
+    if (first + d < last) fetch(slot[d], first + d);
+  int buf = 0;
+#pragma unroll 1
+  for (int s0 = first; s0 < last; s0 += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
       const int span = s0 + d;
       if (span >= last) break;
       // the buffer of the span before the last one: every wave is past the
       // barrier that follows its reads
+      uint32_t* tb = tiles + buf * (MT * kTileWords);
+      buf ^= 1;
 #pragma unroll
       for (int i = 0; i < PX; ++i) {
         if constexpr (sizeof(T) == 2)
-          xp[i].store(tiles[d] + i * kTileWords, tok, piece);
+          slot[d].xp[i].store(tb + i * kTileWords, tok, piece);
         else
-          xp[i].store(tiles[d] + (tok >> 2) * kTileWords, tok & 3, piece);
+          slot[d].xp[i].store(tb + (tok >> 2) * kTileWords, tok & 3, piece);
       }
-      if (span + 1 < last) fetch(slot[d ^ 1], span + 1);
+      if (span + D - 1 < last) fetch(slot[(d + D - 1) % D], span + D - 1);
       __syncthreads();
-      span_product<BITS, MODE, MT, NT>(tiles[d], slot[d].cw, slot[d].sc, slot[d].zo,
+      span_product<BITS, MODE, MT, NT>(tb, slot[d].cw, slot[d].sc, slot[d].zo,
                                        a.K - span * kSpan < kSpan, mask, ones, lr, lq, acc);
     }
   }
-  float* out = a.part + static_cast<int64_t>(blockIdx.z) * a.tokens * a.N;
+  float* out = a.part + static_cast<int64_t>(slice) * a.tokens * a.N;
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -738,25 +810,25 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
     }
 }
 
-// y = the slices' sums and the nonzeros of 16 rows of F, for up to 64 tokens
-template <typename T>
+// y = the slices' sums and the nonzeros of 8 RPW rows of F, for up to 64 tokens
+template <typename T, int RPW>
 __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
                                                                  T* __restrict__ y) {
-  constexpr int TB = 64;
-  __shared__ float ad[16][TB + 4];
+  constexpr int TB = 64, RB = 8 * RPW;
+  __shared__ float ad[RB][TB + 4];
   __shared__ uint2 ent[kEntries];
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * RB;
   if (a.row_ptr != nullptr) {
-    const int k0 = a.row_ptr[n0], kend = a.row_ptr[min(n0 + 16, a.N)];
-    const int row = n0 + (threadIdx.x >> 5);
+    const int k0 = a.row_ptr[n0], kend = a.row_ptr[min(n0 + RB, a.N)];
+    const int row = n0 + threadIdx.x / (64 / RPW);
     const int beg = a.row_ptr[min(row, a.N)], end = a.row_ptr[min(row + 1, a.N)];
     Entries en;
     en.load(a, k0, kend);
-    nonzeros<2, false>(a, en, ent, k0, kend, beg, end, 0, a.tp / 4, nullptr, ad);
+    nonzeros<RPW, false>(a, en, ent, k0, kend, beg, end, a.tp / 4, nullptr, ad);
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < a.tokens * 16; e += kThreads) {
-    const int t = e >> 4, n = e & 15;
+  for (int e = threadIdx.x; e < a.tokens * RB; e += kThreads) {
+    const int t = e / RB, n = e % RB;
     if (n0 + n >= a.N) continue;
     const int64_t at = static_cast<int64_t>(t) * a.N + n0 + n;
     float v = 0.f;
@@ -767,13 +839,28 @@ __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
 }
 
 // ---- launches
+template <typename T>
+hipError_t finish(const DecodeArgs& a, T* y, hipStream_t s) {
+  constexpr int RPW = 1;
+  hipLaunchKernelGGL((decode_finish_kernel<T, RPW>), dim3((a.N + 8 * RPW - 1) / (8 * RPW)),
+                     dim3(kThreads), 0, s, a, y);
+  return hipGetLastError();
+}
+
+size_t z_lds(const DecodeArgs& a) {
+  return a.z_blocks > 0 ? static_cast<size_t>(a.z_cols + a.z_cols / 16) * 4 : 0;
+}
+
 template <int BITS, int MODE, int NT, typename T, bool FEW, bool LOCAL>
 hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
-  const dim3 grid((a.N + 16 * NT - 1) / (16 * NT));
-  const size_t lds = LOCAL ? static_cast<size_t>(a.tokens) * (a.K + a.K / 16) * 4 : 0;
-  hipLaunchKernelGGL((decode_kernel<BITS, MODE, NT, T, FEW, LOCAL>), grid, dim3(kThreads), lds, s,
-                     x, a, y);
-  return hipGetLastError();
+  const size_t staged = MODE == kWide ? static_cast<size_t>(32) * NT * (a.qw.gpr + 1) * 4 : 0;
+  const size_t local = LOCAL ? static_cast<size_t>(a.tokens) * (a.K + a.K / 16) * 4 : 0;
+  const size_t lds = staged + local > z_lds(a) ? staged + local : z_lds(a);
+  hipLaunchKernelGGL((decode_kernel<BITS, MODE, NT, T, FEW, LOCAL>),
+                     dim3(a.z_blocks + (a.N + 16 * NT - 1) / (16 * NT)), dim3(kThreads), lds, s, x,
+                     a, y);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess && a.part != nullptr ? finish(a, y, s) : e;
 }
 
 // tokens few enough for the transform in LDS
@@ -783,12 +870,12 @@ template <int BITS, int MODE, typename T>
 hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   if (a.tokens > Rows<T>::TOK) {
     constexpr int TB = Rows<T>::TOK * kWideTiles;
-    const dim3 grid((a.N + kWideRows - 1) / kWideRows, (a.tokens + TB - 1) / TB, a.slices);
-    hipLaunchKernelGGL((decode_wide_kernel<BITS, MODE, T>), grid, dim3(kWideThreads), 0, s, x, a);
+    const int blocks = (a.N + kWideRows - 1) / kWideRows * ((a.tokens + TB - 1) / TB) * a.slices;
+    const size_t tiles = sizeof(uint32_t) * 2 * kWideTiles * kTileWords;
+    hipLaunchKernelGGL((decode_wide_kernel<BITS, MODE, T>), dim3(a.z_blocks + blocks),
+                       dim3(kWideThreads), tiles > z_lds(a) ? tiles : z_lds(a), s, x, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((decode_finish_kernel<T>), dim3((a.N + 15) / 16), dim3(kThreads), 0, s, a, y);
-    return hipGetLastError();
+    return e == hipSuccess ? finish(a, y, s) : e;
   }
   if (a.tokens <= 4) {
     if (a.row_ptr != nullptr && is_local(a.tokens, a.K))
@@ -838,12 +925,14 @@ int wide_slices(int K, int N) {
 struct DecodeWs {
   size_t part, total;     // zt at 0
 };
+// Calls of both types find room: fp32 ones take decode_wide_kernel from 5 tokens
+// on, bf16 ones from 17.
 DecodeWs decode_ws(int T, int K, int N, int64_t p) {
   DecodeWs l;
-  l.part = p > 0 && !is_local(T, K) ? static_cast<size_t>(K) * padded_tokens(T) * 4 : 0;
-  l.total = l.part;
-  // fp32 calls take the wide kernel from 5 tokens on, bf16 ones from 17
-  if (T > Rows<float>::TOK) l.total += static_cast<size_t>(wide_slices(K, N)) * T * N * 4;
+  const bool z = p > 0 && !is_local(T, K);
+  l.part = z ? static_cast<size_t>(K) * padded_tokens(T) * 4 : 0;
+  const size_t sums = static_cast<size_t>(T) * N * 4;
+  l.total = l.part + (T > Rows<float>::TOK ? wide_slices(K, N) * sums : z ? sums : 0);
   return l;
 }
 
@@ -864,22 +953,20 @@ hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N
   a.E = E;
   a.c = c;
   a.log_b = log_n;
-  a.part = reinterpret_cast<float*>(static_cast<char*>(scratch) + decode_ws(T, a.K, N, p).part);
-  a.slices = wide_slices(a.K, N);
+  const bool wide = T > (dt == Dt::F32 ? Rows<float>::TOK : Rows<uint16_t>::TOK);
   const bool through_memory = p > 0 && !is_local(T, a.K);
-  a.zt = through_memory ? static_cast<float*>(scratch) : nullptr;
+  a.part = wide || through_memory
+               ? reinterpret_cast<float*>(static_cast<char*>(scratch) + decode_ws(T, a.K, N, p).part)
+               : nullptr;
+  a.slices = wide ? wide_slices(a.K, N) : 1;
+  a.z_out = static_cast<float*>(scratch);
+  a.zt = a.z_out;
+  // whole blocks of columns, 2048 together at least, in one workgroup
+  a.z_cols = log_n >= 11 ? 1 << log_n : 2048;
+  a.z_blocks = through_memory ? T * ((a.K + a.z_cols - 1) / a.z_cols) : 0;
   a.alpha = through_memory ? alpha : alpha / static_cast<float>(1 << log_n);
-  auto go = [&](auto* xx, auto* yy) {
-    if (through_memory) {
-      hipLaunchKernelGGL((decode_z_kernel<std::remove_const_t<std::remove_pointer_t<decltype(yy)>>>), dim3(T), dim3(kThreads), (a.K + a.K / 16) * sizeof(float),
-                         s, xx, a.K, log_n, a.tp, static_cast<float*>(scratch));
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    return decode_d(xx, a, yy, s);
-  };
-  if (dt == Dt::F32) return go(static_cast<const float*>(x), static_cast<float*>(y));
-  return go(static_cast<const uint16_t*>(x), static_cast<uint16_t*>(y));
+  if (dt == Dt::F32) return decode_d(static_cast<const float*>(x), a, static_cast<float*>(y), s);
+  return decode_d(static_cast<const uint16_t*>(x), a, static_cast<uint16_t*>(y), s);
 }
 
 }  // namespace qwha
