@@ -250,7 +250,9 @@ struct DecodeArgs {
   const float* c;
   float alpha;                 // alpha / b for the plain sums of a transform in LDS
   int log_b;
-  float* part;                 // partial sums [slices][tokens][N], where a finishing pass follows
+  // partial sums, where a finishing pass follows: [slices][ceil(N / 16)][tokens]
+  // [16], so that it reads the 16 rows it finishes as one run of memory
+  float* part;
   int slices;
   float* z_out;                // zt, written by the launch's first z_blocks workgroups
   int z_cols, z_blocks;        // columns of a token that one of them transforms
@@ -276,6 +278,11 @@ struct Groups {
     }
   }
 };
+
+__device__ __forceinline__ int64_t part_at(const DecodeArgs& a, int slice, int t, int n) {
+  const int64_t tiles = (a.N + 15) >> 4;
+  return ((slice * tiles + (n >> 4)) * a.tokens + t) * 16 + (n & 15);
+}
 
 // The product of one span: acc += s (x (OFF + q) - (OFF + z) sum x), group by
 // group. Lane l's results: W's row l % 16 of tile j and the token rows
@@ -441,16 +448,17 @@ __device__ __forceinline__ void write_z(const T* __restrict__ x, const DecodeArg
 // kEntries of them are fetched beside whatever comes first and wait in LDS, so
 // that only the gather of z is left; each further round's are fetched while the
 // one before is worked on. 64 / RPW lanes take a row.
-constexpr int kEntries = 4 * kThreads;
+constexpr int kEntriesEach = 8;                 // per thread: fewer rounds beat fewer registers
+constexpr int kEntries = kEntriesEach * kThreads;
 constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
 constexpr int kLocalTokens = 4;
 
 struct Entries {
-  uint2 e[4];                            // column, value
+  uint2 e[kEntriesEach];                            // column, value
   __device__ __forceinline__ void load(const DecodeArgs& a, int kb, int kend) {
     if (kend <= kb) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kEntriesEach; ++i) {
       const int64_t at =
           static_cast<int64_t>(kb) + min(i * kThreads + static_cast<int>(threadIdx.x), kend - kb - 1);
       e[i] = uint2{static_cast<uint32_t>(a.E[2 * at + 1]), __float_as_uint(a.c[at])};
@@ -458,7 +466,7 @@ struct Entries {
   }
   __device__ __forceinline__ void store(uint2* ent) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ent[i * kThreads + threadIdx.x] = e[i];
+    for (int i = 0; i < kEntriesEach; ++i) ent[i * kThreads + threadIdx.x] = e[i];
   }
 };
 
@@ -679,12 +687,11 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) v += __uint_as_float(own[i][t * LD + n]);
-    const int64_t at = static_cast<int64_t>(t) * a.N + n0 + n;
     if (!LOCAL && a.part != nullptr) {
-      a.part[at] = v;
+      a.part[part_at(a, 0, t, n0 + n)] = v;
     } else {
       if constexpr (LOCAL) v = fmaf(a.alpha, ad[n][t], v);
-      Elem<T>::st(y, at, v);
+      Elem<T>::st(y, static_cast<int64_t>(t) * a.N + n0 + n, v);
     }
   }
 }
@@ -697,6 +704,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
 constexpr int kWideThreads = 256;
 constexpr int kWideRows = 128;
 constexpr int kWideTiles = 4;
+constexpr int kWideGroups = 32;    // groups of a slice whose steps and zeros LDS holds
 
 template <int BITS, int MODE, typename T>
 __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* __restrict__ x,
@@ -723,6 +731,26 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
   const int first = static_cast<int>(static_cast<int64_t>(spans) * slice / a.slices);
   const int last = static_cast<int>(static_cast<int64_t>(spans) * (slice + 1) / a.slices);
 
+  // steps and zeros of the slice's groups for the workgroup's rows, in LDS
+  const int g0 = first * kSpan >> a.qw.lg_group;
+  const int ng = min((last * kSpan - 1 >> a.qw.lg_group) + 1, a.qw.gpr) - g0;
+  float* steps = dyn + 2 * kWideTiles * kTileWords;
+  float* zeros = steps + kWideRows * (kWideGroups + 1);
+  const bool staged = ng <= kWideGroups;
+  if (staged) {
+    const int rows = min(kWideRows, a.N - bn * kWideRows);
+    const float* s = a.qw.scales + static_cast<int64_t>(bn) * kWideRows * a.qw.gpr + g0;
+    const float* z = a.qw.zeros + static_cast<int64_t>(bn) * kWideRows * a.qw.gpr + g0;
+    const int g = tid & (kWideGroups - 1);
+    if (g < ng) {
+#pragma unroll 4
+      for (int r = tid / kWideGroups; r < rows; r += kWideThreads / kWideGroups) {
+        steps[r * (kWideGroups + 1) + g] = s[r * a.qw.gpr + g];
+        zeros[r * (kWideGroups + 1) + g] = z[r * a.qw.gpr + g];
+      }
+    }
+  }
+
   const int nb = min(n0, a.N - 1);                      // waves past N repeat the last row
   const uint32_t* ctile = a.qw.codes + static_cast<int64_t>(nb) * a.qw.wpr;
   const float* stile = a.qw.scales + static_cast<int64_t>(nb) * a.qw.gpr;
@@ -744,15 +772,25 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
     Groups<G> sc[NT], zo[NT];
     Piece<T> xp[PX];
   } slot[D];
-  auto fetch = [&](Slot& s, int span) {
-    const int c0 = span * kSpan;
+  // Every workgroup starts at a span of its own. In step they would all read the
+  // same columns, and rows a power of two apart meet in few of the L2's
+  // channels.
+  const int count = last - first, turn = (bn + slice) % max(count, 1);
+  auto span_at = [&](int i) {
+    const int r = i + turn;
+    return first + (r < count ? r : r - count);
+  };
+  auto fetch = [&](Slot& s, int i) {
+    const int span = span_at(i), c0 = span * kSpan;
 #pragma unroll
     for (int i = 0; i < PX; ++i) s.xp[i].load(x, xoff[i], min(c0 + 8 * piece, a.K - 8));
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       s.cw[j].load(ctile, coff[j], min(c0 + 32 * lq, a.K - 32));
-      s.sc[j].load(stile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
-      s.zo[j].load(ztile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
+      if (!staged) {
+        s.sc[j].load(stile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
+        s.zo[j].load(ztile, soff[j], c0 >> a.qw.lg_group, a.qw.gpr);
+      }
     }
   };
   const uint32_t mask = in_vgpr(Code::MASK);
@@ -764,14 +802,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int d = 0; d < D - 1; ++d)
-    if (first + d < last) fetch(slot[d], first + d);
+    if (d < count) fetch(slot[d], d);
   int buf = 0;
 #pragma unroll 1
-  for (int s0 = first; s0 < last; s0 += D) {
+  for (int i0 = 0; i0 < count; i0 += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int span = s0 + d;
-      if (span >= last) break;
+      if (i0 + d >= count) break;
       // the buffer of the span before the last one: every wave is past the
       // barrier that follows its reads
       uint32_t* tb = tiles + buf * (MT * kTileWords);
@@ -783,13 +820,25 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
         else
           slot[d].xp[i].store(tb + (tok >> 2) * kTileWords, tok & 3, piece);
       }
-      if (span + D - 1 < last) fetch(slot[(d + D - 1) % D], span + D - 1);
+      if (i0 + d + D - 1 < count) fetch(slot[(d + D - 1) % D], i0 + d + D - 1);
       __syncthreads();
+      if (staged) {
+        const int g = (span_at(i0 + d) * kSpan >> a.qw.lg_group) - g0;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int at = (w * 32 + j * 16 + lr) * (kWideGroups + 1);
+#pragma unroll
+          for (int k = 0; k < G; ++k) {
+            slot[d].sc[j].v[k] = steps[at + min(g + k, ng - 1)];
+            slot[d].zo[j].v[k] = zeros[at + min(g + k, ng - 1)];
+          }
+        }
+      }
       span_product<BITS, MODE, MT, NT>(tb, slot[d].cw, slot[d].sc, slot[d].zo,
-                                       a.K - span * kSpan < kSpan, mask, ones, lr, lq, acc);
+                                       a.K - span_at(i0 + d) * kSpan < kSpan, mask, ones, lr, lq,
+                                       acc);
     }
   }
-  float* out = a.part + static_cast<int64_t>(slice) * a.tokens * a.N;
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -800,12 +849,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int t = t0 + i * 16 + 4 * lq + r;
-          if (t < a.tokens) out[static_cast<int64_t>(t) * a.N + n] = acc[i][j][r];
+          if (t < a.tokens) a.part[part_at(a, slice, t, n)] = acc[i][j][r];
         }
       } else {
         const int t = t0 + i * 4 + lq;
         if (t < a.tokens)
-          out[static_cast<int64_t>(t) * a.N + n] = acc[i][j][0] + acc[i][j][1] + acc[i][j][2];
+          a.part[part_at(a, slice, t, n)] = acc[i][j][0] + acc[i][j][1] + acc[i][j][2];
       }
     }
 }
@@ -814,8 +863,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
 template <typename T, int RPW>
 __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
                                                                  T* __restrict__ y) {
-  constexpr int TB = 64, RB = 8 * RPW;
-  __shared__ float ad[RB][TB + 4];
+  constexpr int RB = 8 * RPW;
+  __shared__ float ad[RB][64 + 4];
   __shared__ uint2 ent[kEntries];
   const int n0 = blockIdx.x * RB;
   if (a.row_ptr != nullptr) {
@@ -827,23 +876,37 @@ __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
     nonzeros<RPW, false>(a, en, ent, k0, kend, beg, end, a.tp / 4, nullptr, ad);
     __syncthreads();
   }
+  const int64_t step = static_cast<int64_t>((a.N + 15) >> 4) * a.tokens * 16;
   for (int e = threadIdx.x; e < a.tokens * RB; e += kThreads) {
     const int t = e / RB, n = e % RB;
     if (n0 + n >= a.N) continue;
-    const int64_t at = static_cast<int64_t>(t) * a.N + n0 + n;
+    const float* p = a.part + part_at(a, 0, t, n0 + n);
     float v = 0.f;
-    for (int i = 0; i < a.slices; ++i) v += a.part[static_cast<int64_t>(i) * a.tokens * a.N + at];
+    int i = 0;
+#pragma unroll 1
+    for (; i + 8 <= a.slices; i += 8, p += 8 * step) {     // 8 reads on their way
+      float q[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] = p[k * step];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += q[k];
+    }
+#pragma unroll 2
+    for (; i < a.slices; ++i, p += step) v += *p;
     if (a.row_ptr != nullptr) v = fmaf(a.alpha, ad[n][t], v);
-    Elem<T>::st(y, at, v);
+    Elem<T>::st(y, static_cast<int64_t>(t) * a.N + n0 + n, v);
   }
 }
 
 // ---- launches
 template <typename T>
 hipError_t finish(const DecodeArgs& a, T* y, hipStream_t s) {
-  constexpr int RPW = 1;
-  hipLaunchKernelGGL((decode_finish_kernel<T, RPW>), dim3((a.N + 8 * RPW - 1) / (8 * RPW)),
-                     dim3(kThreads), 0, s, a, y);
+  // 8 rows each until 16 are enough for two workgroups per compute unit
+  if (a.N < 8192)
+    hipLaunchKernelGGL((decode_finish_kernel<T, 1>), dim3((a.N + 7) / 8), dim3(kThreads), 0, s, a, y);
+  else
+    hipLaunchKernelGGL((decode_finish_kernel<T, 2>), dim3((a.N + 15) / 16), dim3(kThreads), 0, s, a,
+                       y);
   return hipGetLastError();
 }
 
@@ -871,7 +934,8 @@ hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   if (a.tokens > Rows<T>::TOK) {
     constexpr int TB = Rows<T>::TOK * kWideTiles;
     const int blocks = (a.N + kWideRows - 1) / kWideRows * ((a.tokens + TB - 1) / TB) * a.slices;
-    const size_t tiles = sizeof(uint32_t) * 2 * kWideTiles * kTileWords;
+    const size_t tiles = sizeof(uint32_t) * 2 * kWideTiles * kTileWords +
+                         sizeof(float) * 2 * kWideRows * (kWideGroups + 1);
     hipLaunchKernelGGL((decode_wide_kernel<BITS, MODE, T>), dim3(a.z_blocks + blocks),
                        dim3(kWideThreads), tiles > z_lds(a) ? tiles : z_lds(a), s, x, a);
     const hipError_t e = hipGetLastError();
@@ -914,12 +978,14 @@ int padded_tokens(int T) {
   return tp;
 }
 
-// Workgroups that share the spans of 128 rows: enough of them for two per
-// compute unit, at least two spans each.
-int wide_slices(int K, int N) {
+// Workgroups that share the spans of 128 rows: with those that write z (one or
+// more a token) two per compute unit, which is what fits at once, so that none
+// waits for a second turn; at least two spans each.
+int wide_slices(int z_blocks, int K, int N) {
   const int tiles = (N + kWideRows - 1) / kWideRows, spans = (K + kSpan - 1) / kSpan;
-  const int want = (512 + tiles - 1) / tiles, most = spans / 2 > 0 ? spans / 2 : 1;
-  return want < most ? want : most;
+  const int want = (512 - z_blocks) / tiles, most = spans / 2;
+  const int n = want < most ? want : most;
+  return n < 1 ? 1 : n;
 }
 
 struct DecodeWs {
@@ -931,8 +997,8 @@ DecodeWs decode_ws(int T, int K, int N, int64_t p) {
   DecodeWs l;
   const bool z = p > 0 && !is_local(T, K);
   l.part = z ? static_cast<size_t>(K) * padded_tokens(T) * 4 : 0;
-  const size_t sums = static_cast<size_t>(T) * N * 4;
-  l.total = l.part + (T > Rows<float>::TOK ? wide_slices(K, N) * sums : z ? sums : 0);
+  const size_t sums = static_cast<size_t>(T) * ((N + 15) / 16 * 16) * 4;
+  l.total = l.part + (T > Rows<float>::TOK ? wide_slices(z ? T : 0, K, N) * sums : z ? sums : 0);
   return l;
 }
 
@@ -958,7 +1024,7 @@ hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N
   a.part = wide || through_memory
                ? reinterpret_cast<float*>(static_cast<char*>(scratch) + decode_ws(T, a.K, N, p).part)
                : nullptr;
-  a.slices = wide ? wide_slices(a.K, N) : 1;
+  a.slices = wide ? wide_slices(through_memory ? T : 0, a.K, N) : 1;
   a.z_out = static_cast<float*>(scratch);
   a.zt = a.z_out;
   // whole blocks of columns, 2048 together at least, in one workgroup
