@@ -9,7 +9,7 @@
 // tokens in turn, each with its own running maximum and sum of the softmax.
 // Both products run on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16):
 //   scores  A: 16 rows = 4 query heads x (upper, middle, lower 8 bits of the
-//           fp32 query's mantissa, nothing); B: 16 tokens' codes. Lane l holds
+//           fp32 query's mantissa, unused); B: 16 tokens' codes. Lane l holds
 //           token l % 16 and a quarter of its row;
 //   values  A: the weights p s_v, split alike; B: for each of N / 16 columns j
 //           the codes of column (N / 16) (l % 16) + j of 8 tokens: a lane reads
@@ -63,14 +63,20 @@ __device__ __forceinline__ float quarter_sum(float v) {
   return v + lane_xor<8>(v);
 }
 
-// part `r` (0: upper, 1: middle, 2: lower, 3: nothing) of 8 fp32 numbers
-__device__ __forceinline__ bf16x8 part_operand(const float* f, int r) {
+// A lane's part of fp32 numbers: what is left after taking off the upper 8 bits
+// of mantissa (`first` lanes: 0xFFFF0000) and the next 8 (`second` lanes), cut to
+// bf16. Without branches; rows of no part hold a copy that nobody reads.
+struct PartMask {
+  uint32_t first, second;
+  __device__ __forceinline__ explicit PartMask(int part)
+      : first(part >= 1 ? 0xFFFF0000u : 0u), second(part >= 2 ? 0xFFFF0000u : 0u) {}
+};
+__device__ __forceinline__ bf16x8 part_operand(const float* f, PartMask m) {
   uint32_t x[8], d[4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint32_t h[3];
-    split3(f[i], h);
-    x[i] = r == 0 ? h[0] : r == 1 ? h[1] : r == 2 ? h[2] : 0u;
+    const float r = f[i] - __uint_as_float(__float_as_uint(f[i]) & m.first);
+    x[i] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & m.second));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
@@ -161,6 +167,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   }
   __syncthreads();
 
+  const PartMask pm(lr & 3);
   bf16x8 qf[HT][STEPS];
   float qsum[HT];
 #pragma unroll
@@ -170,7 +177,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 8 + i];
-      qf[t][s] = part_operand(f, lr & 3);
+      qf[t][s] = part_operand(f, pm);
     }
     float sum = 0.f;
 #pragma unroll
@@ -291,7 +298,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
       const float4* p = reinterpret_cast<const float4*>(&ps[t][lr >> 2][8 * lq]);
       const float4 p0v = p[0], p1v = p[1];
       const float f[8] = {p0v.x, p0v.y, p0v.z, p0v.w, p1v.x, p1v.y, p1v.z, p1v.w};
-      pf[t] = part_operand(f, lr & 3);
+      pf[t] = part_operand(f, pm);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
