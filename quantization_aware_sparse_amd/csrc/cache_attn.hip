@@ -7,19 +7,24 @@
 // A workgroup takes one key/value head of one sequence, up to 4 HT of the query
 // heads that read it, and a slice of the tokens; its waves take tiles of 32
 // tokens in turn, each with its own running maximum and sum of the softmax.
-// Both products run on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16):
-//   scores  A: 16 rows = 4 query heads x (upper, middle, lower 8 bits of the
-//           fp32 query's mantissa, unused); B: 16 tokens' codes. Lane l holds
-//           token l % 16 and a quarter of its row;
-//   values  A: the weights p s_v, split alike; B: for each of N / 16 columns j
-//           the codes of column (N / 16) (l % 16) + j of 8 tokens: a lane reads
-//           its N / 16 columns of 8 tokens and pairs the tokens' codes up.
-// Codes enter as 2^bits + q (4 bits) or q (8 bits), all exact in bf16, and the
-// rest of (q - z) is taken off in fp32: with OFF = 16 or 0
-//   score   = s_k (sum q' (OFF + code) - (OFF + z_k) sum q'),
+//   scores  on the 8-bit integer matrix cores (v_mfma_i32_16x16x64_i8), exact.
+//           A: 16 rows = 4 query heads x (upper, middle, lower digit, unused):
+//           q' as a 24-bit fixed-point number of the head's own power of two, in
+//           three signed digits of 8 bits; B: 16 tokens' codes (8-bit ones less
+//           128). Codes need a mask and a shift to be operands, as bf16 a
+//           permutation and an or of each pair as well. Lane l holds token
+//           l % 16 and a quarter of its row;
+//   values  on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16). A: the weights
+//           p s_v as three bf16 numbers that sum to them exactly; B: for each of
+//           N / 16 columns j the codes of column (N / 16) (l % 16) + j of 8
+//           tokens: a lane reads its N / 16 columns of 8 tokens and pairs the
+//           tokens' codes up, as 16 + q (4 bits) or q (8 bits), exact in bf16.
+// What is constant in (q - z) is taken off in fp32:
+//   score   = s_k (sum q' code' + (0 or 128 - z_k) sum q'),
 //   output  = sum p s_v (OFF + code) - sum p s_v (OFF + z_v).
-// So every product is exact and only fp32 additions round. The three parts of a
-// head lie in one lane's results.
+// A head's three parts lie in one lane's results.
+// Bound by the vector units, which unpack: about 250 instructions of a wave for
+// 32 tokens of 128 columns, 9 KB of 4-bit keys and values.
 //
 // cache_combine_kernel joins the slices: one maximum, one sum, one transform.
 #include "cache.h"
@@ -109,18 +114,22 @@ __device__ __forceinline__ void finish_row(const float* o, int u, int rotate, T*
   store16(out + u * 16, v);
 }
 
-template <int N, int BITS, int HT, typename T>
+// ONE_PAGE: a tile lies in one page (of 32 tokens or more), whose address the
+// whole wave shares.
+template <int N, int BITS, int HT, bool ONE_PAGE, typename T>
 __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __restrict__ q,
                                                                      Cache c, AttnArgs a,
                                                                      T* __restrict__ out) {
   constexpr int HEADS = 4 * HT;
-  constexpr int STEPS = N / 32;                     // matrix instructions of a score
+  constexpr int STEPS = N / 64;                     // matrix instructions of a score
   constexpr int KW = N / 4 * BITS / 32;             // words of a quarter of a row
   constexpr int J = N / 16;                         // columns of a lane
   constexpr int VB = J * BITS / 8;                  // bytes of them
   constexpr int VW = VB >= 4 ? VB / 4 : 1;
   constexpr int ROW = N * BITS / 8;                 // bytes of a row
-  constexpr float OFF = BITS == 4 ? 16.f : 0.f;
+  constexpr float OFF = BITS == 4 ? 16.f : 0.f;     // in the values' operands
+  constexpr float KOFF = BITS == 4 ? 0.f : 128.f;   // taken off the keys'
+
   constexpr int PLD = kTile + 4;
   __shared__ __attribute__((aligned(16))) float qs[HEADS][N];
   __shared__ __attribute__((aligned(16))) float om[kAttnWaves][HEADS][N];
@@ -168,25 +177,54 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   __syncthreads();
 
   const PartMask pm(lr & 3);
-  bf16x8 qf[HT][STEPS];
-  float qsum[HT];
+  // digits of the queries: q' = 2^(e - 22) Q with 2^e above the head's largest
+  // |q'|, Q = (d0 256 + d1) 256 + d2. Lane l: row l % 16 = (head, digit), the
+  // columns of its quarter in the order of the codes' operands.
+  i32x4 qf[HT][STEPS];
+  float qunit[HT], qsum[HT];                        // of head lq: 2^(e - 22), sum of Q
 #pragma unroll
   for (int t = 0; t < HT; ++t) {
+    auto largest = [&](int head) {
+      float top = 0.f;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 8 + i];
-      qf[t][s] = part_operand(f, pm);
-    }
+      for (int i = 0; i < J; ++i) top = fmaxf(top, fabsf(qs[head][lr * J + i]));
+      return quarter_max(top);
+    };
+    // the maximum of head t * 4 + lq is at hand in quarter lq, that of the
+    // lane's row, head lr / 4, in quarter lr / 4
+    const float top = largest(t * 4 + lq);
+    const int e = top > 0.f ? ilogbf(top) + 1 : 0;
+    qunit[t] = ldexpf(1.f, max(e, -100) - 22);
+    const float unit = ldexpf(1.f, 22 - max(__shfl(e, (lr >> 2) * 16), -100));
     float sum = 0.f;
+    const float inv = ldexpf(1.f, 22 - max(e, -100));
 #pragma unroll
-    for (int i = 0; i < J; ++i) sum += qs[t * 4 + lq][lr * J + i];
+    for (int i = 0; i < J; ++i) sum += rintf(qs[t * 4 + lq][lr * J + i] * inv);
     qsum[t] = quarter_sum(sum);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint32_t x = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // column of byte i of register r: 4-bit words give their even codes
+          // first, then their odd ones
+          const int at = BITS == 4 ? r / 2 * 8 + 2 * i + r % 2 : r * 4 + i;
+          const int v = static_cast<int>(
+              rintf(qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 16 + at] * unit));
+          const int d2 = static_cast<int8_t>(v), v1 = (v - d2) >> 8;
+          const int d1 = static_cast<int8_t>(v1), d0 = (v1 - d1) >> 8;
+          const int d = (lr & 3) == 0 ? d0 : (lr & 3) == 1 ? d1 : d2;
+          x |= static_cast<uint32_t>(d & 0xFF) << (8 * i);
+        }
+        qf[t][s][r] = static_cast<int>(x);
+      }
   }
 
   const uint32_t mask = in_vgpr(kMask4);
   const f32x4 zero4 = f32x4{0.f, 0.f, 0.f, 0.f};
+  const i32x4 izero4 = i32x4{0, 0, 0, 0};
   const int64_t vals = c.part_rows();
   const uint32_t in_page = (1u << c.lg_page) - 1;
   f32x4 acc[HT][J];
@@ -210,7 +248,36 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
     *live = t < len && g >= 0;
     return c.row_in(0, g < 0 ? 0 : g, static_cast<int>(t & in_page), h);
   };
+  const uint32_t koff = lr * ROW + lq * (ROW / 4), voff = 8 * lq * ROW + lr * VB;
+  auto fetch_page = [&](Tile& x, uint32_t tile) {
+    const uint32_t t = tile * kTile;
+    const int32_t g = __builtin_amdgcn_readfirstlane(tab[(t >> c.lg_page) - p0]);
+    const int64_t r = c.row_in(0, g < 0 ? 0 : g, static_cast<int>(t & in_page), h);
+    const char* kp = reinterpret_cast<const char*>(c.codes) + r * ROW;
+    const char* vp = kp + vals * ROW;
+    const float *sp = c.scales + r, *zp = c.zeros + r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x.live[i] = g >= 0 && t + 16 * i + lr < len;
+      load_words<KW>(kp + (koff + 16 * i * ROW), x.k[i]);
+      x.sk[i] = sp[16 * i + lr];
+      x.zk[i] = zp[16 * i + lr];
+      x.sv[i] = (sp + vals)[16 * i + lr];
+      x.zv[i] = (zp + vals)[16 * i + lr];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (VB >= 4)
+        load_words<VW>(vp + (voff + i * ROW), x.v[i]);
+      else
+        x.v[i][0] = *reinterpret_cast<const uint16_t*>(vp + (voff + i * ROW));
+    }
+  };
   auto fetch = [&](Tile& x, uint32_t tile) {
+    if constexpr (ONE_PAGE) {
+      fetch_page(x, tile);
+      return;
+    }
     const char* codes = reinterpret_cast<const char*>(c.codes);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -240,19 +307,24 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
     Tile next;
     if (tile + kAttnWaves < last) fetch(next, tile + kAttnWaves);
 
-    f32x4 sg[HT][2];
+    i32x4 sg[HT][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
-        bf16x8 kf;
-        if constexpr (BITS == 4)
-          kf = operand4(cur.k[i][s], mask);
-        else
-          kf = operand8(cur.k[i][2 * s], cur.k[i][2 * s + 1]);
+        i32x4 kf;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (BITS == 4) {
+            const uint32_t w = cur.k[i][2 * s + r / 2];
+            kf[r] = static_cast<int>((r % 2 ? w >> 4 : w) & 0x0F0F0F0Fu);
+          } else {
+            kf[r] = static_cast<int>(cur.k[i][4 * s + r] ^ 0x80808080u);
+          }
+        }
 #pragma unroll
         for (int t = 0; t < HT; ++t)
-          sg[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[t][s], kf, s ? sg[t][i] : zero4, 0, 0, 0);
+          sg[t][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qf[t][s], kf, s ? sg[t][i] : izero4, 0, 0, 0);
       }
     // what lies in a place that is left out is never used, whatever it holds
     float sv[2], ov[2];
@@ -266,8 +338,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
       float s[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float d = sg[t][i][0] + sg[t][i][1] + sg[t][i][2];
-        const float x = cur.sk[i] * fmaf(-(OFF + cur.zk[i]), qsum[t], d);
+        const float d = fmaf(65536.f, static_cast<float>(sg[t][i][0]),
+                             fmaf(256.f, static_cast<float>(sg[t][i][1]),
+                                  static_cast<float>(sg[t][i][2])));
+        const float x = cur.sk[i] * qunit[t] * fmaf(KOFF - cur.zk[i], qsum[t], d);
         s[i] = cur.live[i] ? x : -INFINITY;
       }
       const float mn = fmaxf(m[t], quarter_max(fmaxf(s[0], s[1])));
@@ -471,14 +545,19 @@ hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cac
     constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
     auto go = [&](auto* qq, auto* oo) {
       using T = std::remove_pointer_t<decltype(oo)>;
+      auto run = [&](auto tiles, auto one_page) {
+        hipLaunchKernelGGL((cache_attn_kernel<N, BITS, decltype(tiles)::value,
+                                              decltype(one_page)::value, T>),
+                           grid, dim3(kAttnThreads), 0, s, qq, c, a, oo);
+      };
+      auto by_page = [&](auto tiles) {
+        if (c.lg_page >= 5) run(tiles, std::true_type{});
+        else run(tiles, std::false_type{});
+      };
       if constexpr (N <= 128) {
-        if (ht == 2)
-          hipLaunchKernelGGL((cache_attn_kernel<N, BITS, 2, T>), grid, dim3(kAttnThreads), 0, s,
-                             qq, c, a, oo);
+        if (ht == 2) by_page(std::integral_constant<int, 2>{});
       }
-      if (ht == 1)
-        hipLaunchKernelGGL((cache_attn_kernel<N, BITS, 1, T>), grid, dim3(kAttnThreads), 0, s, qq,
-                           c, a, oo);
+      if (ht == 1) by_page(std::integral_constant<int, 1>{});
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess || a.slices == 1) return e;
       hipLaunchKernelGGL((cache_combine_kernel<N, T>), dim3(static_cast<unsigned>(B) * q_heads),

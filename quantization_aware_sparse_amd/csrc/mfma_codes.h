@@ -7,6 +7,7 @@ namespace qwha {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // (x & mask) | bits in one instruction, where the mask is in a vector register
 // (one scalar operand per instruction). Left to the compiler: it knows the wait
