@@ -16,6 +16,9 @@ from typing import Dict, Optional
 import torch
 
 from ._lib import QwhaError, check, lib  # noqa: F401
+from . import _binding
+
+_binding.set_error(QwhaError)
 
 __all__ = [
     "QWHA_F32", "QWHA_BF16", "QwhaError", "lib",
@@ -207,76 +210,18 @@ def qwha_layer_fwd(x: torch.Tensor, codes, scales, zeros, bits: int, group: int,
 
 
 # ---------------------------------------------------------------- decoding
-def _given(dev: int, dtype, shape, name: str, t: torch.Tensor) -> int:
-    """The address of an argument of the decoding calls, checked: a contiguous
-    tensor of this type and shape on the call's device (its index; -1: the CPU)."""
-    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on the call's device ({dev})")
-    raise ValueError("tensors must be contiguous")
-
-
-# The current stream's handle alone: torch.cuda.current_stream makes an object of
-# it, which costs half as much as a launch.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _enqueue(dev: int, where: str, fn, *args) -> None:
-    """Calls fn on the current stream of the tensors' device, which need not
-    be the current device."""
-    if dev < 0:
-        raise ValueError("tensors must live on the GPU")
-    if dev == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
-    if status != 0:
-        check(status, where)
-
-
+# These calls are short, and Python's share of them would be the larger part: the
+# checks of types, shapes and devices, the outputs, the workspace and the stream
+# (the current one of the tensors' device, which need not be the current device)
+# are the compiled binding's. Wrong types raise TypeError, wrong shapes, devices
+# or strides ValueError, what the library refuses QwhaError.
 def qwha_layer_decode(x: torch.Tensor, codes, scales, zeros, bits: int, group: int, row_ptr=None,
                       E=None, c=None, alpha: float = 1.0, y: Optional[torch.Tensor] = None,
                       ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """qwha_layer_fwd for the few tokens of a decoding step: y = x W_Q^T + alpha
     z F^T for x [T][d_in], T <= QWHA_DECODE_MAX_T, bf16 or fp32 (y alike).
     Without an adapter (c None or empty) the base layer alone."""
-    T, d_in = x.shape
-    dev = x.get_device()
-    d_out, groups = scales.shape
-    if bits not in (2, 3, 4, 8):
-        raise ValueError(f"bits={bits} is not one of 2, 3, 4, 8")
-    if groups * group != d_in:
-        raise ValueError(f"scales {tuple(scales.shape)} do not hold {d_in} columns in groups of "
-                         f"{group}")
-    cpw = 32 // bits
-    p = 0 if c is None else c.numel()
-    args = (_given(dev, torch.int32, (d_out, -(-d_in // cpw)), "codes", codes),
-            _given(dev, torch.float32, (d_out, groups), "scales", scales),
-            _given(dev, torch.float32, (d_out, groups), "zeros", zeros), bits, group, p)
-    if p:
-        args += (_given(dev, torch.int32, (d_out + 1,), "row_ptr", row_ptr),
-                 _given(dev, torch.int32, (p, 2), "E", E),
-                 _given(dev, torch.float32, (p,), "c", c))
-    else:
-        args += (None, None, None)
-    if y is None:
-        y = x.new_empty((T, d_out))
-    if ws is None:
-        need = lib.qwha_layer_decode_workspace_bytes(T, d_in, d_out, p)
-        if need:
-            ws = workspace(need, x.device)
-    _enqueue(dev, "qwha_layer_decode", lib.qwha_layer_decode,
-             _given(dev, x.dtype, (T, d_in), "x", x) if T else None, _dt(x), T, d_in, d_out, *args,
-             float(alpha), _given(dev, x.dtype, (T, d_out), "y", y) if T else None,
-             ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0)
-    return y
+    return _binding.layer_decode(x, codes, scales, zeros, bits, group, row_ptr, E, c, alpha, y, ws)
 
 
 def qwha_cache_empty(n_pages: int, heads: int, page: int, head_dim: int, bits: int, device):
@@ -289,53 +234,23 @@ def qwha_cache_empty(n_pages: int, heads: int, page: int, head_dim: int, bits: i
             torch.zeros(at, dtype=torch.float32, device=device))
 
 
-def _cache_args(dev, codes, scales, zeros, heads: int, head_dim: int, bits: int):
-    """(addresses, n_pages, page) of a cache that holds such rows."""
-    if codes.dim() != 5:
-        raise ValueError("codes must be [2][n_pages][heads][page][words]")
-    _, n_pages, _, page, _ = codes.shape
-    at = (2, n_pages, heads, page)
-    return ((_given(dev, torch.int32, (*at, head_dim * bits // 32), "codes", codes),
-             _given(dev, torch.float32, at, "scales", scales),
-             _given(dev, torch.float32, at, "zeros", zeros)), n_pages, page)
-
-
 def qwha_cache_write(k: torch.Tensor, v: torch.Tensor, slots, codes, scales, zeros, bits: int,
                      rotate: bool = True) -> None:
     """Quantizes k and v [T][heads][head_dim] (fp32 or bf16) into the slots
     (int32 [T], page * page_size + offset; others, as -1, are skipped) of a
     cache made by qwha_cache_empty; with rotate through the Walsh-Hadamard
     transform of each row."""
-    T, heads, head_dim = k.shape
-    dev = k.get_device()
-    arrays, n_pages, page = _cache_args(dev, codes, scales, zeros, heads, head_dim, bits)
-    _enqueue(dev, "qwha_cache_write", lib.qwha_cache_write,
-             _given(dev, k.dtype, k.shape, "k", k) if T else None,
-             _given(dev, k.dtype, k.shape, "v", v) if T else None, _dt(k), T,
-             _given(dev, torch.int32, (T,), "slots", slots) if T else None, heads, head_dim, bits,
-             int(rotate), n_pages, page, *arrays)
+    _binding.cache_write(k, v, slots, codes, scales, zeros, bits, rotate)
 
 
 def qwha_cache_read(codes, scales, zeros, slots, bits: int, head_dim: int, rotate: bool = True,
                     out_dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
                     v: Optional[torch.Tensor] = None):
-    """k and v [T][heads][head_dim] of the slots (int32 [T]) of a cache; zeros
-    for slots outside it."""
-    dev = codes.get_device()
-    heads = codes.shape[2]
-    T = slots.numel()
-    arrays, n_pages, page = _cache_args(dev, codes, scales, zeros, heads, head_dim, bits)
-    shape = (T, heads, head_dim)
-    if k is None:
-        k = codes.new_empty(shape, dtype=out_dtype)
-    if v is None:
-        v = k.new_empty(shape)
-    _enqueue(dev, "qwha_cache_read", lib.qwha_cache_read, *arrays, heads, head_dim, bits,
-             int(rotate), n_pages, page,
-             _given(dev, torch.int32, (T,), "slots", slots) if T else None, T, _dt(k),
-             _given(dev, k.dtype, shape, "k", k) if T else None,
-             _given(dev, k.dtype, shape, "v", v) if T else None)
-    return k, v
+    """k and v [T][heads][head_dim] of the slots (int32 [T]) of a cache, in
+    out_dtype (bf16 or fp32) or in the given k and v; zeros for slots outside
+    it."""
+    return _binding.cache_read(codes, scales, zeros, slots, bits, head_dim, rotate,
+                               _DT[out_dtype] == QWHA_F32, k, v)
 
 
 def qwha_cache_attn(q: torch.Tensor, codes, scales, zeros, table, lens, bits: int,
@@ -346,26 +261,7 @@ def qwha_cache_attn(q: torch.Tensor, codes, scales, zeros, table, lens, bits: in
     or bf16, the output alike), over the first lens[b] tokens of the pages
     table[b] (int32 [B] and [B][width]) of a cache; scale 1/sqrt(head_dim)
     unless given."""
-    B, q_heads, head_dim = q.shape
-    dev = q.get_device()
-    heads = codes.shape[2]
-    arrays, n_pages, page = _cache_args(dev, codes, scales, zeros, heads, head_dim, bits)
-    width = table.shape[1]
-    if out is None:
-        out = torch.empty_like(q)
-    if ws is None:
-        need = lib.qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
-        if need:
-            ws = workspace(need, q.device)
-    _enqueue(dev, "qwha_cache_attn", lib.qwha_cache_attn,
-             _given(dev, q.dtype, q.shape, "q", q) if B else None, _dt(q), B, q_heads, *arrays,
-             heads, head_dim, bits, int(rotate), n_pages, page,
-             _given(dev, torch.int32, (B, width), "table", table) if B else None, width,
-             _given(dev, torch.int32, (B,), "lens", lens) if B else None,
-             head_dim ** -0.5 if scale is None else float(scale),
-             _given(dev, q.dtype, q.shape, "out", out) if B else None,
-             ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0)
-    return out
+    return _binding.cache_attn(q, codes, scales, zeros, table, lens, bits, rotate, scale, out, ws)
 
 
 # ---------------------------------------------------------------- materialize

@@ -1,4 +1,5 @@
-"""Builds libqwha.so (all HIP kernels + the C-ABI) for gfx950 with hipcc.
+"""Builds libqwha.so (all HIP kernels + the C-ABI) for gfx950 with hipcc, and
+_binding.so (the decoding calls' Python binding) with the host compiler.
 
 Usage: python quantization_aware_sparse_amd/build.py (run by path: importing the
 package loads the built library)
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libqwha.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["api.hip", "cache.hip", "cache_attn.hip", "decode.hip", "fwht.hip", "init.hip",
            "materialize.hip", "quant.hip", "refine.hip", "select_global.hip", "spmm.hip"]
@@ -46,19 +48,56 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """The binding's object, against the installed torch's headers and ABI."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    rocm = os.path.dirname(os.path.dirname(hipcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wall",
+           "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"host compiler failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-fPIC", "-o", tmp, obj, "-L" + HERE,
+           "-l:libqwha.so", "-L" + lib, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", "8")))
+    jobs = min(len(SOURCES) + 1, int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {BINDING}")
     return LIB
 
 
