@@ -438,58 +438,56 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   }
 }
 
-// One query head of one sequence: its slices, joined. N / 16 lanes hold a
-// slice's sums; the workgroup's 16 * 256 / N such groups take the slices in turn.
+// One query head of one sequence: its slices, joined. N / 16 lanes read a slice's
+// sums beside its maximum and sum; the workgroup's 16 * 256 / N such groups take
+// the slices in turn, each with its own running maximum: one way to memory, and
+// the groups meet in LDS.
 template <int N, typename T>
 __global__ __launch_bounds__(kAttnThreads) void cache_combine_kernel(AttnArgs a,
                                                                      T* __restrict__ out) {
   constexpr int J = N / 16, GROUPS = kAttnThreads / J;
   __shared__ float os[GROUPS][N + 4];
-  __shared__ float tops[kAttnWaves], sums[GROUPS];
+  __shared__ float2 gml[GROUPS];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, u = tid % J, g = tid / J;
-  const float2* ml = a.ml + row * a.slices;
-  float top = -INFINITY;
-  for (int s = tid; s < a.slices; s += kAttnThreads) top = fmaxf(top, ml[s].x);
-  top = quarter_max(top);
-  top = fmaxf(top, __shfl_xor(top, 16));
-  top = fmaxf(top, __shfl_xor(top, 32));
-  if ((tid & 63) == 0) tops[tid >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kAttnWaves; ++i) top = fmaxf(top, tops[i]);
-  float v[16], sum = 0.f;
+  float v[16], top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int r = 0; r < 16; ++r) v[r] = 0.f;
-  if (top > -INFINITY) {
-    for (int s = g; s < a.slices; s += GROUPS) {
-      const float2 x = ml[s];
-      if (!(x.y > 0.f)) continue;                  // a slice without tokens
-      const float f = exp2_fast(x.x - top);
-      sum = fmaf(f, x.y, sum);
-      const float4* p = reinterpret_cast<const float4*>(a.part + (row * a.slices + s) * N + u * 16);
+  for (int s = g; s < a.slices; s += GROUPS) {
+    const float2 x = a.ml[row * a.slices + s];
+    const float4* p = reinterpret_cast<const float4*>(a.part + (row * a.slices + s) * N + u * 16);
+    float4 o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 o = p[i];
-        v[4 * i] = fmaf(f, o.x, v[4 * i]);
-        v[4 * i + 1] = fmaf(f, o.y, v[4 * i + 1]);
-        v[4 * i + 2] = fmaf(f, o.z, v[4 * i + 2]);
-        v[4 * i + 3] = fmaf(f, o.w, v[4 * i + 3]);
-      }
+    for (int i = 0; i < 4; ++i) o[i] = p[i];
+    if (!(x.y > 0.f)) continue;                    // a slice without tokens: nothing written
+    const float mn = fmaxf(top, x.x), keep = exp2_fast(top - mn), f = exp2_fast(x.x - mn);
+    top = mn;
+    sum = fmaf(f, x.y, sum * keep);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[4 * i] = fmaf(f, o[i].x, v[4 * i] * keep);
+      v[4 * i + 1] = fmaf(f, o[i].y, v[4 * i + 1] * keep);
+      v[4 * i + 2] = fmaf(f, o[i].z, v[4 * i + 2] * keep);
+      v[4 * i + 3] = fmaf(f, o[i].w, v[4 * i + 3] * keep);
     }
   }
 #pragma unroll
   for (int r = 0; r < 16; ++r) os[g][u * 16 + r] = v[r];
-  if (u == 0) sums[g] = sum;
+  if (u == 0) gml[g] = float2{top, sum};
   __syncthreads();
   const int used = min(GROUPS, a.slices);
   if (tid < N) {
+    top = -INFINITY;
+    for (int i = 0; i < used; ++i) top = fmaxf(top, gml[i].x);
     float o = 0.f, l = 0.f;
-    for (int i = 0; i < used; ++i) {
-      o += os[i][tid];
-      l += sums[i];
+    if (top > -INFINITY) {
+      for (int i = 0; i < used; ++i) {
+        const float f = exp2_fast(gml[i].x - top);
+        o = fmaf(f, os[i][tid], o);
+        l = fmaf(f, gml[i].y, l);
+      }
     }
-    os[0][tid] = l > 0.f ? o / l : 0.f;
+    os[0][tid] = l > 0.f ? o / l : 0.f;            // column tid is this thread's alone
   }
   __syncthreads();
   if (tid < J) finish_row<N>(os[0], u, a.rotate, out + row * N);
