@@ -228,12 +228,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   const int64_t vals = c.part_rows();
   const uint32_t in_page = (1u << c.lg_page) - 1;
   f32x4 acc[HT][J];
-  float m[HT], l[HT], zacc[HT];
+  float m[HT], l[HT];
 #pragma unroll
   for (int t = 0; t < HT; ++t) {
     m[t] = -INFINITY;
     l[t] = 0.f;
-    zacc[t] = 0.f;
 #pragma unroll
     for (int j = 0; j < J; ++j) acc[t][j] = zero4;
   }
@@ -349,21 +348,27 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
       if (__any(mn > m[t])) {
         const float keep = exp2_fast(m[t] - at);
         l[t] *= keep;
-        zacc[t] *= keep;
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[t][j][r] *= keep;
         m[t] = mn;
       }
+      float zs = 0.f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float p = exp2_fast(s[i] - at);
         l[t] += p;
         const float pv = p * sv[i];
-        zacc[t] = fmaf(pv, ov[i], zacc[t]);
+        zs = fmaf(pv, ov[i], zs);
         ps[t][lq][16 * i + lr] = pv;
       }
+      // sum p s_v (OFF + z_v) comes off tile by tile, ahead of the tile's product:
+      // what adds up over the tokens is then the output itself, and not the far
+      // larger sums that it is the difference of
+      zs = quarter_sum(zs);
+#pragma unroll
+      for (int j = 0; j < J; ++j) acc[t][j][0] -= zs;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     bf16x8 pf[HT];
@@ -403,10 +408,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   // the waves' sums, joined
 #pragma unroll
   for (int t = 0; t < HT; ++t) {
-    const float zs = quarter_sum(zacc[t]), ls = quarter_sum(l[t]);
+    const float ls = quarter_sum(l[t]);
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      om[w][t * 4 + lq][lr * J + j] = acc[t][j][0] + acc[t][j][1] + acc[t][j][2] - zs;
+      om[w][t * 4 + lq][lr * J + j] = acc[t][j][0] + acc[t][j][1] + acc[t][j][2];
     if (lr == 0) wml[w][t * 4 + lq] = float2{m[t], ls};
   }
   __syncthreads();

@@ -243,6 +243,7 @@ struct Piece<float> {
 
 struct DecodeArgs {
   int tokens, K, N, tp;
+  int64_t p;
   QuantW qw;
   const float* zt;             // zt[column][tp], where z goes through memory
   const int32_t* row_ptr;      // null without an adapter
@@ -447,11 +448,13 @@ __device__ __forceinline__ void write_z(const T* __restrict__ x, const DecodeArg
 // ---- the nonzeros of some rows of F: side by side in E and c. The first
 // kEntries of them are fetched beside whatever comes first and wait in LDS, so
 // that only the gather of z is left; each further round's are fetched while the
-// one before is worked on. 64 / RPW lanes take a row.
+// one before is worked on. 64 / RPW lanes take a row, or with SPLIT all waves one
+// row, each its share.
 constexpr int kEntriesEach = 8;                 // per thread: fewer rounds beat fewer registers
 constexpr int kEntries = kEntriesEach * kThreads;
 constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
 constexpr int kLocalTokens = 4;
+constexpr int kLongRow = 512;            // nonzeros of a row, on average
 
 struct Entries {
   uint2 e[kEntriesEach];                            // column, value
@@ -487,17 +490,18 @@ __device__ __forceinline__ float lanes_sum(float v, int from) {
   return v;
 }
 
-// ad[row][token] for the workgroup's 8 RPW rows. LOCAL: z in LDS, a lane a
-// nonzero, its tokens one after the other; else lpn lanes hold 4 tokens each of
-// a nonzero's column. All threads call it.
-template <int RPW, bool LOCAL, int LDA>
+// ad[row][token] for the workgroup's 8 RPW rows (SPLIT: ad[wave][token], to be
+// added up). LOCAL: z in LDS, a lane a nonzero, its tokens one after the other;
+// else lpn lanes hold 4 tokens each of a nonzero's column. All threads call it.
+template <int RPW, bool LOCAL, bool SPLIT, int LDA>
 __device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2* ent, int k0,
                                          int kend, int beg, int end, int lpn, const float* zl,
                                          float (*ad)[LDA]) {
   constexpr int LPR = 64 / RPW;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int in_row = lane & (LPR - 1);
-  const int npw = LPR / lpn, sub = in_row / lpn;
+  const int npw = (SPLIT ? kDecodeWaves : 1) * (LPR / lpn);
+  const int sub = in_row / lpn + (SPLIT ? w * (LPR / lpn) : 0);
   const float* zg = a.zt + (in_row & (lpn - 1)) * 4;
   const int zld = zpad(a.K);
   f32x4 s4 = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -679,7 +683,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
       red[lq * LD + j * 16 + lr] = acc[0][j][0] + acc[0][j][1] + acc[0][j][2];
     }
   }
-  if constexpr (LOCAL) nonzeros<RPW, true>(a, en, ent, k0, kend, beg, end, 1, zl, ad);
+  if constexpr (LOCAL) nonzeros<RPW, true, false>(a, en, ent, k0, kend, beg, end, 1, zl, ad);
   __syncthreads();
   for (int e = threadIdx.x; e < a.tokens * 16 * NT; e += kThreads) {
     const int t = e / (16 * NT), n = e % (16 * NT);
@@ -859,21 +863,23 @@ __global__ __launch_bounds__(kWideThreads, 2) void decode_wide_kernel(const T* _
     }
 }
 
-// y = the slices' sums and the nonzeros of 8 RPW rows of F, for up to 64 tokens
-template <typename T, int RPW>
+// y = the slices' sums and the nonzeros of 8 RPW rows of F (SPLIT: of one), for up
+// to 64 tokens
+template <typename T, int RPW, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
                                                                  T* __restrict__ y) {
-  constexpr int RB = 8 * RPW;
-  __shared__ float ad[RB][64 + 4];
+  static_assert(!SPLIT || RPW == 1, "a row takes whole waves");
+  constexpr int RB = SPLIT ? 1 : 8 * RPW;
+  __shared__ float ad[8 * RPW][64 + 4];
   __shared__ uint2 ent[kEntries];
   const int n0 = blockIdx.x * RB;
   if (a.row_ptr != nullptr) {
     const int k0 = a.row_ptr[n0], kend = a.row_ptr[min(n0 + RB, a.N)];
-    const int row = n0 + threadIdx.x / (64 / RPW);
+    const int row = SPLIT ? n0 : n0 + threadIdx.x / (64 / RPW);
     const int beg = a.row_ptr[min(row, a.N)], end = a.row_ptr[min(row + 1, a.N)];
     Entries en;
     en.load(a, k0, kend);
-    nonzeros<RPW, false>(a, en, ent, k0, kend, beg, end, a.tp / 4, nullptr, ad);
+    nonzeros<RPW, false, SPLIT>(a, en, ent, k0, kend, beg, end, a.tp / 4, nullptr, ad);
     __syncthreads();
   }
   const int64_t step = static_cast<int64_t>((a.N + 15) >> 4) * a.tokens * 16;
@@ -893,7 +899,13 @@ __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
     }
 #pragma unroll 2
     for (; i < a.slices; ++i, p += step) v += *p;
-    if (a.row_ptr != nullptr) v = fmaf(a.alpha, ad[n][t], v);
+    if (a.row_ptr != nullptr) {
+      float f = ad[n][t];
+      if constexpr (SPLIT)
+#pragma unroll
+        for (int k = 1; k < kDecodeWaves; ++k) f += ad[k][t];
+      v = fmaf(a.alpha, f, v);
+    }
     Elem<T>::st(y, static_cast<int64_t>(t) * a.N + n0 + n, v);
   }
 }
@@ -901,13 +913,17 @@ __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
 // ---- launches
 template <typename T>
 hipError_t finish(const DecodeArgs& a, T* y, hipStream_t s) {
-  // 8 rows each until 16 are enough for two workgroups per compute unit
-  if (a.N < 8192)
-    hipLaunchKernelGGL((decode_finish_kernel<T, 1>), dim3((a.N + 7) / 8), dim3(kThreads), 0, s, a, y);
-  else
-    hipLaunchKernelGGL((decode_finish_kernel<T, 2>), dim3((a.N + 15) / 16), dim3(kThreads), 0, s, a,
-                       y);
-  return hipGetLastError();
+  auto go = [&](auto kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3((a.N + rows - 1) / rows), dim3(kThreads), 0, s, a, y);
+    return hipGetLastError();
+  };
+  // Rows per workgroup by what keeps the chip busy: one where there are few rows
+  // or they are long (43 rows of 8096 nonzeros: 317 us with 16 a workgroup), 8
+  // until 16 are enough for two workgroups per compute unit.
+  if (a.row_ptr != nullptr && (a.N < 2048 || a.p / a.N > kLongRow))
+    return go(decode_finish_kernel<T, 1, true>, 1);
+  if (a.N < 8192) return go(decode_finish_kernel<T, 1, false>, 8);
+  return go(decode_finish_kernel<T, 2, false>, 16);
 }
 
 size_t z_lds(const DecodeArgs& a) {
@@ -926,8 +942,11 @@ hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   return e == hipSuccess && a.part != nullptr ? finish(a, y, s) : e;
 }
 
-// tokens few enough for the transform in LDS
-bool is_local(int T, int K) { return T <= kLocalTokens && T * K <= kLocal; }
+// tokens few enough for the transform in LDS, rows of F short enough for one
+// workgroup's 16
+bool is_local(int T, int K, int N, int64_t p) {
+  return p > 0 && T <= kLocalTokens && T * K <= kLocal && p / N <= kLongRow;
+}
 
 template <int BITS, int MODE, typename T>
 hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
@@ -942,7 +961,7 @@ hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
     return e == hipSuccess ? finish(a, y, s) : e;
   }
   if (a.tokens <= 4) {
-    if (a.row_ptr != nullptr && is_local(a.tokens, a.K))
+    if (is_local(a.tokens, a.K, a.N, a.p))
       return decode_t<BITS, MODE, 1, T, true, true>(x, a, y, s);
     return decode_t<BITS, MODE, 1, T, true, false>(x, a, y, s);
   }
@@ -995,7 +1014,7 @@ struct DecodeWs {
 // on, bf16 ones from 17.
 DecodeWs decode_ws(int T, int K, int N, int64_t p) {
   DecodeWs l;
-  const bool z = p > 0 && !is_local(T, K);
+  const bool z = p > 0 && !is_local(T, K, N, p);
   l.part = z ? static_cast<size_t>(K) * padded_tokens(T) * 4 : 0;
   const size_t sums = static_cast<size_t>(T) * ((N + 15) / 16 * 16) * 4;
   l.total = l.part + (T > Rows<float>::TOK ? wide_slices(z ? T : 0, K, N) * sums : z ? sums : 0);
@@ -1020,7 +1039,8 @@ hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N
   a.c = c;
   a.log_b = log_n;
   const bool wide = T > (dt == Dt::F32 ? Rows<float>::TOK : Rows<uint16_t>::TOK);
-  const bool through_memory = p > 0 && !is_local(T, a.K);
+  const bool through_memory = p > 0 && !is_local(T, a.K, N, p);
+  a.p = p;
   a.part = wide || through_memory
                ? reinterpret_cast<float*>(static_cast<char*>(scratch) + decode_ws(T, a.K, N, p).part)
                : nullptr;
