@@ -177,9 +177,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   __syncthreads();
 
   const PartMask pm(lr & 3);
-  // digits of the queries: q' = 2^(e - 22) Q with 2^e above the head's largest
-  // |q'|, Q = (d0 256 + d1) 256 + d2. Lane l: row l % 16 = (head, digit), the
-  // columns of its quarter in the order of the codes' operands.
+  // digits of the queries: q' = 2^(e - 23) Q with 0.99 * 2^e above the head's
+  // largest |q'|, so that Q = (d0 256 + d1) 256 + d2 in digits of -128 .. 127.
+  // Lane l: row l % 16 = (head, digit), the columns of its quarter in the order
+  // of the codes' operands.
   i32x4 qf[HT][STEPS];
   float qunit[HT], qsum[HT];                        // of head lq: 2^(e - 22), sum of Q
 #pragma unroll
@@ -193,11 +194,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
     // the maximum of head t * 4 + lq is at hand in quarter lq, that of the
     // lane's row, head lr / 4, in quarter lr / 4
     const float top = largest(t * 4 + lq);
-    const int e = top > 0.f ? ilogbf(top) + 1 : 0;
-    qunit[t] = ldexpf(1.f, max(e, -100) - 22);
-    const float unit = ldexpf(1.f, 22 - max(__shfl(e, (lr >> 2) * 16), -100));
+    int e = 0;
+    if (frexpf(top, &e) > 0.99f) ++e;
+    e = max(e, -100);
+    qunit[t] = ldexpf(1.f, e - 23);
+    const float unit = ldexpf(1.f, 23 - __shfl(e, (lr >> 2) * 16));
     float sum = 0.f;
-    const float inv = ldexpf(1.f, 22 - max(e, -100));
+    const float inv = ldexpf(1.f, 23 - e);
 #pragma unroll
     for (int i = 0; i < J; ++i) sum += rintf(qs[t * 4 + lq][lr * J + i] * inv);
     qsum[t] = quarter_sum(sum);
