@@ -462,7 +462,8 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   bytes (0 when out of range), 256-byte aligned; calls that may overlap
  *   need one each.
  * Values read (k, v, q, and the cache's rows in use) must be finite, as for
- * every call here; others spoil their own rows only. Out-of-range slots and
+ * every call here, and so must fp32(hi - lo) (with `rotate` it is, as |v| and
+ * hi - lo are at most the largest |x|); others spoil their own rows only. Out-of-range slots and
  * pages are checked on the device and never read or written through.
  * --------------------------------------------------------------------------- */
 qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64_t T,
@@ -508,10 +509,10 @@ typedef enum qwha_kernel {
   QWHA_KERNEL_REFINE = 14,      /* the per-row solves of qwha_refine_values */
   QWHA_KERNEL_MERGE = 15,       /* qwha_merge */
   QWHA_KERNEL_QGEMM = 16,       /* the base GEMM inside qwha_layer_fwd */
-  QWHA_KERNEL_LAYER_DECODE = 17, /* the product inside qwha_layer_decode */
+  QWHA_KERNEL_LAYER_DECODE = 17, /* qwha_layer_decode, all its launches */
   QWHA_KERNEL_CACHE_WRITE = 18, /* qwha_cache_write */
   QWHA_KERNEL_CACHE_READ = 19,  /* qwha_cache_read */
-  QWHA_KERNEL_CACHE_ATTN = 20   /* qwha_cache_attn */
+  QWHA_KERNEL_CACHE_ATTN = 20   /* qwha_cache_attn, all its launches */
 } qwha_kernel;
 qwha_status qwha_profile_next(int32_t kernel, hipEvent_t start, hipEvent_t stop);
 

@@ -249,6 +249,8 @@ def qwha_cache_read(codes, scales, zeros, slots, bits: int, head_dim: int, rotat
     """k and v [T][heads][head_dim] of the slots (int32 [T]) of a cache, in
     out_dtype (bf16 or fp32) or in the given k and v; zeros for slots outside
     it."""
+    if out_dtype not in _DT:
+        raise TypeError(f"unsupported dtype {out_dtype}")
     return _binding.cache_read(codes, scales, zeros, slots, bits, head_dim, rotate,
                                _DT[out_dtype] == QWHA_F32, k, v)
 

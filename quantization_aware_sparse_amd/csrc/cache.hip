@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict_
       for (int i = 0; i < PER / 16; ++i) load16(src + 16 * i, a + 16 * i);
       fwht_lanes<N, PER>(a, u);
 #pragma unroll
-      for (int r = 0; r < PER; ++r) f[r] = static_cast<float>(a[r]) * (1.f / N);   // a power of two
+      for (int r = 0; r < PER; ++r) f[r] = static_cast<float>(a[r] * (1. / N));   // the sum may pass fp32's range
     } else {
 #pragma unroll
       for (int i = 0; i < PER / 16; ++i) load16(src + 16 * i, f + 16 * i);

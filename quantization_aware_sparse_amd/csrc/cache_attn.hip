@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   // Lane l: row l % 16 = (head, digit), the columns of its quarter in the order
   // of the codes' operands.
   i32x4 qf[HT][STEPS];
-  float qunit[HT], qsum[HT];                        // of head lq: 2^(e - 22), sum of Q
+  float qunit[HT], qsum[HT];                        // of head lq: 2^(e - 23), sum of Q
 #pragma unroll
   for (int t = 0; t < HT; ++t) {
     auto largest = [&](int head) {
@@ -456,7 +456,7 @@ __global__ __launch_bounds__(kAttnThreads) void cache_combine_kernel(AttnArgs a,
   constexpr int J = N / 16, GROUPS = kAttnThreads / J;
   __shared__ float os[GROUPS][N + 4];
   __shared__ float2 gml[GROUPS];
-  const int64_t row = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.y) * a.q_heads + blockIdx.x;
   const int tid = threadIdx.x, u = tid % J, g = tid / J;
   float v[16], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -566,7 +566,8 @@ hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cac
       if (ht == 1) by_page(std::integral_constant<int, 1>{});
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess || a.slices == 1) return e;
-      hipLaunchKernelGGL((cache_combine_kernel<N, T>), dim3(static_cast<unsigned>(B) * q_heads),
+      hipLaunchKernelGGL((cache_combine_kernel<N, T>),
+                         dim3(static_cast<unsigned>(q_heads), static_cast<unsigned>(B)),
                          dim3(kAttnThreads), 0, s, a, oo);
       return hipGetLastError();
     };

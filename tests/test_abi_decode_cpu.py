@@ -149,6 +149,8 @@ def test_binding_refusals():
         lib.qwha_cache_write(k, k[:2], slots, *cache, 4)
     with pytest.raises(ValueError, match="GPU"):
         lib.qwha_cache_read(*cache, slots, 4, 64)
+    with pytest.raises(TypeError, match="dtype"):
+        lib.qwha_cache_read(*cache, slots, 4, 64, out_dtype=torch.float16)
     table = torch.zeros(3, 2, dtype=torch.int32)
     with pytest.raises(ValueError, match="GPU"):
         lib.qwha_cache_attn(k, *cache, table, slots, 4)

@@ -135,6 +135,34 @@ def test_write_on_the_border_between_two_codes(q, bits):
     assert np.array_equal(host(arrays[2])[1, 0, 0, :6], zz[:, 0])
 
 
+@pytest.mark.parametrize("dim,bits", [(64, 4), (128, 8), (256, 4)])
+def test_write_and_read_at_the_ends_of_fp32(q, dim, bits):
+    # rows whose sums pass fp32's range though their mean does not, and rows
+    # beside its lowest normal numbers. Read back s times a whole number below
+    # 2^24 is rounded once, so it is the oracle's value, rounded
+    say("ends of fp32", dim, bits)
+    rng = np.random.default_rng(dim + bits)
+    x = rng.uniform(-1, 1, (6, 1, dim)).astype(np.float32)
+    x[0] = 1.0
+    x[1] = -1.0
+    x[:3] *= np.float32(1.9 * 2.0 ** 126)
+    x[3] *= np.float32(2.0 ** -118)
+    x[4] *= np.float32(2.0 ** -122)
+    x[5] *= np.float32(2.0 ** -140)
+    arrays = q.qwha_cache_empty(1, 1, 8, dim, bits, DEV)
+    t, slots = to_dev(x), to_dev(np.arange(6, dtype=np.int32))
+    q.qwha_cache_write(t, t, slots, *arrays, bits)
+    k, _ = q.qwha_cache_read(*arrays, slots, bits, dim, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    qc, ss, zz = O.cache_quantize(x, bits, True)
+    want = np.zeros((2, 1, 1, 8, dim), dtype=np.uint8)
+    want[:, 0, 0, :6] = qc[:, 0]
+    assert np.array_equal(host(arrays[1])[0, 0, 0, :6], ss[:, 0])
+    assert np.array_equal(host(arrays[2])[1, 0, 0, :6], zz[:, 0])
+    assert torch.equal(arrays[0], pack(want, bits))
+    assert np.array_equal(host(k), O.cache_dequantize(qc, ss, zz, True).astype(np.float32))
+
+
 READS = [  # T, heads, dim, page, pages, bits, rotate, act
     (1, 1, 64, 8, 1, 4, True, "bf16"), (1, 8, 128, 16, 3, 8, True, "f32"),
     (77, 3, 128, 32, 2, 4, True, "f32"), (130, 2, 256, 16, 7, 8, True, "bf16"),
