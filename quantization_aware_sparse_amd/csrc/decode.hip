@@ -872,33 +872,44 @@ __global__ __launch_bounds__(kThreads) void decode_finish_kernel(DecodeArgs a,
   constexpr int RB = SPLIT ? 1 : 8 * RPW;
   __shared__ float ad[8 * RPW][64 + 4];
   __shared__ uint2 ent[kEntries];
+  constexpr int EACH = RB * 64 / kThreads > 1 ? RB * 64 / kThreads : 1;   // results of a thread
+  constexpr int EARLY = 8;       // slices whose sums are fetched ahead of the nonzeros
   const int n0 = blockIdx.x * RB;
+  const int64_t step = static_cast<int64_t>((a.N + 15) >> 4) * a.tokens * 16;
+  const float* p[EACH];
+  float q[EACH][EARLY];
+  auto fetch = [&] {
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int e = min(static_cast<int>(threadIdx.x) + i * kThreads, a.tokens * RB - 1);
+      p[i] = a.part + part_at(a, 0, e / RB, min(n0 + e % RB, a.N - 1));
+#pragma unroll
+      for (int k = 0; k < EARLY; ++k)
+        if (k < a.slices) q[i][k] = p[i][k * step];
+    }
+  };
   if (a.row_ptr != nullptr) {
     const int k0 = a.row_ptr[n0], kend = a.row_ptr[min(n0 + RB, a.N)];
     const int row = SPLIT ? n0 : n0 + threadIdx.x / (64 / RPW);
     const int beg = a.row_ptr[min(row, a.N)], end = a.row_ptr[min(row + 1, a.N)];
+    fetch();
     Entries en;
     en.load(a, k0, kend);
     nonzeros<RPW, false, SPLIT>(a, en, ent, k0, kend, beg, end, a.tp / 4, nullptr, ad);
     __syncthreads();
+  } else {
+    fetch();
   }
-  const int64_t step = static_cast<int64_t>((a.N + 15) >> 4) * a.tokens * 16;
-  for (int e = threadIdx.x; e < a.tokens * RB; e += kThreads) {
-    const int t = e / RB, n = e % RB;
-    if (n0 + n >= a.N) continue;
-    const float* p = a.part + part_at(a, 0, t, n0 + n);
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int e = threadIdx.x + i * kThreads, t = e / RB, n = e % RB;
+    if (e >= a.tokens * RB || n0 + n >= a.N) continue;
     float v = 0.f;
-    int i = 0;
-#pragma unroll 1
-    for (; i + 8 <= a.slices; i += 8, p += 8 * step) {     // 8 reads on their way
-      float q[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = p[k * step];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v += q[k];
-    }
-#pragma unroll 2
-    for (; i < a.slices; ++i, p += step) v += *p;
+    for (int k = 0; k < EARLY; ++k)
+      if (k < a.slices) v += q[i][k];
+#pragma unroll 4
+    for (int k = EARLY; k < a.slices; ++k) v += p[i][k * step];
     if (a.row_ptr != nullptr) {
       float f = ad[n][t];
       if constexpr (SPLIT)
@@ -919,10 +930,12 @@ hipError_t finish(const DecodeArgs& a, T* y, hipStream_t s) {
   };
   // Rows per workgroup by what keeps the chip busy: one where there are few rows
   // or they are long (43 rows of 8096 nonzeros: 317 us with 16 a workgroup), 8
-  // until 16 are enough for two workgroups per compute unit.
+  // up to two workgroups per compute unit, 16 beyond (4096 columns, T = 16, 128
+  // nonzeros a row, whole call with 8 / 16 / 32 rows: 4096 rows 19.0 / 19.4 / 24.9
+  // us, 5120 rows 23.3 / 21.1 / 25.6, 14336 rows 38.4 / 33.7 / 35.7).
   if (a.row_ptr != nullptr && (a.N < 2048 || a.p / a.N > kLongRow))
     return go(decode_finish_kernel<T, 1, true>, 1);
-  if (a.N < 8192) return go(decode_finish_kernel<T, 1, false>, 8);
+  if (a.N <= 4096) return go(decode_finish_kernel<T, 1, false>, 8);
   return go(decode_finish_kernel<T, 2, false>, 16);
 }
 
