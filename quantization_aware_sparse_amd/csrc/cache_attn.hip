@@ -27,6 +27,8 @@
 // 32 tokens of 128 columns, 9 KB of 4-bit keys and values.
 //
 // cache_combine_kernel joins the slices: one maximum, one sum, one transform.
+#include <algorithm>
+
 #include "cache.h"
 #include "lane_fwht.h"
 #include "mfma_codes.h"
@@ -37,9 +39,12 @@ namespace {
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
+// waves of a workgroup that takes a short sequence alone; 16 need 128 registers
+constexpr int many_waves(int n, int bits, int ht) { return ht == 1 && n * bits <= 512 ? 16 : 8; }
+constexpr int kMaxWaves = 16;
 constexpr int kTile = 32;                           // tokens
 constexpr int kTabPages = 1024;                     // pages a slice holds, at most
-constexpr int kTab = kTabPages + kAttnWaves * kTile / 8 + 1;
+constexpr int kTab = kTabPages + kMaxWaves * kTile / 8 + 1;
 
 struct AttnArgs {
   int q_heads, per, groups;    // query heads per key/value head, in groups of 4 HT
@@ -116,11 +121,11 @@ __device__ __forceinline__ void finish_row(const float* o, int u, int rotate, T*
 
 // ONE_PAGE: a tile lies in one page (of 32 tokens or more), whose address the
 // whole wave shares.
-template <int N, int BITS, int HT, bool ONE_PAGE, typename T>
-__global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __restrict__ q,
+template <int N, int BITS, int HT, bool ONE_PAGE, int WAVES, typename T>
+__global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __restrict__ q,
                                                                      Cache c, AttnArgs a,
                                                                      T* __restrict__ out) {
-  constexpr int HEADS = 4 * HT;
+  constexpr int HEADS = 4 * HT, THREADS = WAVES * 64;
   constexpr int STEPS = N / 64;                     // matrix instructions of a score
   constexpr int KW = N / 4 * BITS / 32;             // words of a quarter of a row
   constexpr int J = N / 16;                         // columns of a lane
@@ -132,8 +137,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
 
   constexpr int PLD = kTile + 4;
   __shared__ __attribute__((aligned(16))) float qs[HEADS][N];
-  __shared__ __attribute__((aligned(16))) float om[kAttnWaves][HEADS][N];
-  __shared__ float2 wml[kAttnWaves][HEADS];
+  __shared__ __attribute__((aligned(16))) float om[WAVES][HEADS][N];
+  __shared__ float2 wml[WAVES][HEADS];
   __shared__ int32_t tab[kTab];
   float (*ps)[4][PLD] = reinterpret_cast<float (*)[4][PLD]>(&om[threadIdx.x >> 6][0][0]);
   static_assert(HT * 4 * PLD <= HEADS * N, "a wave's weights fit its place for results");
@@ -151,7 +156,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   const uint32_t len = static_cast<uint32_t>(asked < 0 ? 0 : asked < cap ? asked : cap);
   const uint32_t tiles = (len + kTile - 1) / kTile;
   uint32_t each = (tiles + a.slices - 1) / a.slices;
-  each = (each + kAttnWaves - 1) & ~(kAttnWaves - 1u);
+  each = (each + WAVES - 1) & ~(WAVES - 1u);
   const uint32_t first = min(static_cast<uint64_t>(slice) * each, static_cast<uint64_t>(tiles));
   const uint32_t last = min(first + each, tiles);
 
@@ -161,7 +166,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
     const uint32_t pages = (len + (1u << c.lg_page) - 1) >> c.lg_page;
     const uint32_t p1 = (last * kTile + (1u << c.lg_page) - 1) >> c.lg_page;
     const int32_t* row = a.table + static_cast<int64_t>(b) * a.width;
-    for (uint32_t p = p0 + tid; p < p1; p += kAttnThreads) {
+    for (uint32_t p = p0 + tid; p < p1; p += THREADS) {
       const int32_t g = p < pages ? row[p] : -1;
       tab[p - p0] = g >= 0 && g < c.n_pages ? g : -1;
     }
@@ -305,9 +310,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
   Tile cur;
   if (first + w < last) fetch(cur, first + w);
 #pragma unroll 1
-  for (uint32_t tile = first + w; tile < last; tile += kAttnWaves) {
+  for (uint32_t tile = first + w; tile < last; tile += WAVES) {
     Tile next;
-    if (tile + kAttnWaves < last) fetch(next, tile + kAttnWaves);
+    if (tile + WAVES < last) fetch(next, tile + WAVES);
 
     i32x4 sg[HT][2];
 #pragma unroll
@@ -418,15 +423,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void cache_attn_kernel(const T* __
     if (lr == 0) wml[w][t * 4 + lq] = float2{m[t], ls};
   }
   __syncthreads();
-  for (int e = tid; e < heads * N; e += kAttnThreads) {
+  for (int e = tid; e < heads * N; e += THREADS) {
     const int head = e / N, d = e % N;
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kAttnWaves; ++i) top = fmaxf(top, wml[i][head].x);
+    for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wml[i][head].x);
     float o = 0.f, sum = 0.f;
     if (top > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < kAttnWaves; ++i) {
+      for (int i = 0; i < WAVES; ++i) {
         const float f = exp2_fast(wml[i][head].x - top);
         o = fmaf(f, om[i][head][d], o);
         sum = fmaf(f, wml[i][head].y, sum);
@@ -505,26 +510,45 @@ __global__ __launch_bounds__(kAttnThreads) void cache_combine_kernel(AttnArgs a,
 // 4 and the columns leave the registers for it.
 int head_tiles(int per, int dim) { return per > 4 && dim <= 128 ? 2 : 1; }
 
-// Slices of a sequence: workgroups for four per compute unit, each with a tile
-// for every wave, and no more pages than its table holds.
-int attn_slices(int B, int q_heads, int heads, int dim, int64_t max_tokens, int page) {
+// How the tokens are shared out. `many`: one workgroup of many waves for a
+// sequence and key/value head, no joining pass. Else slices of a sequence:
+// workgroups of 4 waves for four per compute unit, each with a tile for every
+// wave, and no more pages than its table holds.
+// The joining pass costs 3.5 us and up, while a compute unit alone takes 2 us a
+// round of 512 tokens; the more workgroups there are, the less of the chip the
+// first way leaves idle. Columns 128, 4 bits, 8 x 4 heads, us with one workgroup /
+// with slices:
+//   sequences   tokens  200         1000        2000        4000        8000
+//    1           7.0 / 8.4  11.6 /  8.5  16.0 /  8.8  24.0 /  9.5  39.6 / 12.4
+//   16                   -  12.9 / 15.5  18.1 / 17.9  27.0 / 22.9  46.2 / 39.6
+//   32          7.5 / 11.8  14.3 / 18.8  20.4 / 23.8  36.9 / 40.8  64.9 / 69.3
+// (32 of ragged lengths up to 8000: 50.0 / 48.0, up to 4000: 27.8 / 28.3).
+struct AttnPlan {
+  bool many;
+  int slices;
+};
+
+AttnPlan attn_plan(int B, int q_heads, int heads, int dim, int64_t max_tokens, int page) {
   const int per = q_heads / heads, ht = head_tiles(per, dim);
   const int64_t groups = (per + 4 * ht - 1) / (4 * ht);
   const int64_t pairs = static_cast<int64_t>(B) * heads * groups;
-  const int64_t most = (max_tokens + kAttnWaves * kTile - 1) / (kAttnWaves * kTile);
+  const int64_t one = kAttnWaves * kTile;           // tokens of a round of one workgroup
+  if (max_tokens > one && pairs <= 256 && max_tokens <= std::max<int64_t>(256, pairs * pairs / 16))
+    return {true, 1};
+  const int64_t most = (max_tokens + one - 1) / one;
   const int64_t least = (max_tokens + kTabPages * static_cast<int64_t>(page) - 1) /
                         (kTabPages * static_cast<int64_t>(page));
   int64_t want = pairs > 0 ? (1024 + pairs - 1) / pairs : 1;
   if (want > most) want = most;
   if (want < least) want = least;
-  return static_cast<int>(want < 1 ? 1 : want);
+  return {false, static_cast<int>(want < 1 ? 1 : want)};
 }
 
 }  // namespace
 
 size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t max_tokens,
                                 int page) {
-  const int slices = attn_slices(B, q_heads, heads, dim, max_tokens, page);
+  const int slices = attn_plan(B, q_heads, heads, dim, max_tokens, page).slices;
   if (slices == 1) return 0;
   return static_cast<size_t>(B) * q_heads * slices * (dim + 2) * sizeof(float);
 }
@@ -542,8 +566,9 @@ hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cac
   a.lens = lens;
   a.scale = scale * 1.44269504088896340736f;
   a.rotate = rotate;
-  a.slices = attn_slices(B, q_heads, c.heads, c.dim, static_cast<int64_t>(width) << c.lg_page,
-                         1 << c.lg_page);
+  const AttnPlan plan = attn_plan(B, q_heads, c.heads, c.dim,
+                                  static_cast<int64_t>(width) << c.lg_page, 1 << c.lg_page);
+  a.slices = plan.slices;
   a.part = static_cast<float*>(scratch);
   a.ml = reinterpret_cast<float2*>(a.part + static_cast<int64_t>(B) * q_heads * a.slices * c.dim);
   const dim3 grid(static_cast<unsigned>(c.heads) * a.groups * a.slices, static_cast<unsigned>(B));
@@ -551,10 +576,16 @@ hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cac
     constexpr int N = decltype(n)::value, BITS = decltype(bits)::value;
     auto go = [&](auto* qq, auto* oo) {
       using T = std::remove_pointer_t<decltype(oo)>;
-      auto run = [&](auto tiles, auto one_page) {
+      auto with = [&](auto tiles, auto one_page, auto waves) {
+        constexpr int WAVES = decltype(waves)::value;
         hipLaunchKernelGGL((cache_attn_kernel<N, BITS, decltype(tiles)::value,
-                                              decltype(one_page)::value, T>),
-                           grid, dim3(kAttnThreads), 0, s, qq, c, a, oo);
+                                              decltype(one_page)::value, WAVES, T>),
+                           grid, dim3(WAVES * 64), 0, s, qq, c, a, oo);
+      };
+      auto run = [&](auto tiles, auto one_page) {
+        constexpr int MANY = many_waves(N, BITS, decltype(tiles)::value);
+        if (plan.many) with(tiles, one_page, std::integral_constant<int, MANY>{});
+        else with(tiles, one_page, std::integral_constant<int, kAttnWaves>{});
       };
       auto by_page = [&](auto tiles) {
         if (c.lg_page >= 5) run(tiles, std::true_type{});

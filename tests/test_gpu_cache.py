@@ -314,6 +314,23 @@ def test_attn_of_what_lies_behind_the_sequences(q, bits, dim):
               extra=40, spoil=True)
 
 
+# short tables and many of them: one workgroup of many waves a sequence and head
+ATTN_ALONE = [  # heads, per, dim, page, lens, bits, rotate, act
+    (16, 4, 128, 16, [1000, 0, 1, 513, 512, 511, 33, 900, 2, 777], 4, True, "bf16"),
+    (8, 1, 128, 64, [250], 8, True, "f32"), (2, 8, 64, 8, [249, 256, 1], 8, False, "f32"),
+    (1, 2, 256, 32, [129, 250], 4, True, "bf16"), (1, 1, 64, 1024, [1000] * 130, 4, False, "f32"),
+    (40, 1, 64, 16, [1999, 16, 15, 1025, 0], 4, True, "f32"),
+    (16, 3, 256, 32, [1500, 31, 32, 33, 700, 0, 1, 2, 257, 255, 256, 1024], 8, True, "bf16"),
+    (20, 5, 128, 8, [700, 9, 8, 7, 0, 699], 8, False, "f32")]
+
+
+@pytest.mark.parametrize("heads,per,dim,page,lens,bits,rotate,act", ATTN_ALONE)
+def test_attn_of_short_sequences(q, heads, per, dim, page, lens, bits, rotate, act):
+    say("cache attn, short", heads, per, dim, page, lens[:12], bits, rotate, act)
+    attn_case(q, len(lens), heads, per, dim, page, lens, bits, rotate, act,
+              seed=heads + per + dim + page, spoil=True)
+
+
 def test_attn_scale_and_extreme_scores(q):
     say("scales")
     # with a large scale one token takes all the weight, exp of the rest underflows
