@@ -54,7 +54,9 @@ __device__ __forceinline__ CallRow call_row(const Cache& c, uint32_t row) {
 // (16-bit inputs whose exponents span less than 2^37), so v, its range and
 // every code do not depend on the order of the additions. 32 columns a lane:
 // a stage across lanes costs 3 to 5 instructions a value (two moves, a product
-// and sum), one within a lane a single one.
+// and sum), one within a lane a single one. 8192 tokens of 8 heads of 128 (33.5 MB
+// of bf16 in, 9.4 out): 15.9 us, of which the vector units' 35 instructions a
+// value take 15; at 4.9 TB/s the bytes take 8.8. 32 tokens: 3.8 us.
 constexpr int kWritePer = 32;
 
 template <int N, int BITS, typename TIn, bool ROT>
