@@ -188,19 +188,22 @@ __device__ __forceinline__ void transform_codes(const uint32_t* w, int lane, flo
 
 // Rows [T][2][heads] of the slots, dense; a token without a slot reads as
 // zeros. Bound by HBM's writes: N elements out for N * b / 8 + 8 bytes in.
-// Lane u of a row holds the columns 8u .. + 8 of either half of the row (the
-// transform takes the index bits in any order), so that a store instruction
-// covers whole lines of bf16.
+// Lane u of a row holds 16 bytes of output from each of SEGS places, N / SEGS
+// columns apart (the transform takes the index bits in any order), so that a
+// store instruction covers whole lines.
 // IT rows a lane, their loads in flight together. Calls of many rows take 4 and
 // store past the caches, whose lines the codes then keep: 40000 tokens of 8
 // heads of 128 (209 MB) 49.1 us with one row and plain stores, 46.6 with 4 rows,
-// 34.8 with stores past the caches too.
+// 34.8 with stores past the caches too. With 64 columns a store instruction has
+// but half of each line, which must meet the other half in the cache (16384 tokens
+// of 8 heads of 64 as fp32: 21.0 us past it, 15.1 through it).
 template <int N, int BITS, typename TOut, bool ROT, int IT>
 __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
                                                          const int32_t* __restrict__ slots,
                                                          uint32_t rows, TOut* __restrict__ k,
                                                          TOut* __restrict__ v) {
   constexpr int LPR = N / 16, RPB = 256 / LPR, WORDS = 16 * BITS / 32;
+  constexpr int COLS = 16 / sizeof(TOut), SEGS = 16 / COLS;
   const int u = threadIdx.x % LPR;
   const uint32_t row0 = blockIdx.x * (RPB * IT) + threadIdx.x / LPR;
   uint32_t w[IT][WORDS];
@@ -212,16 +215,13 @@ __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
     const int32_t slot = slots[cr[j].t];
     const bool stored = slot >= 0 && (slot >> c.lg_page) < c.n_pages;
     const int64_t at = c.row(cr[j].part, stored ? slot : 0, cr[j].head);
-    const uint32_t* src = c.codes + at * (N * BITS / 32) + u * (WORDS / 2);
+    using Seg = std::conditional_t<COLS * BITS == 16, uint16_t,
+                                   std::conditional_t<COLS * BITS == 32, uint32_t, uint2>>;
+    const Seg* src = reinterpret_cast<const Seg*>(c.codes + at * (N * BITS / 32)) + u;
+    Seg seg[SEGS];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (BITS == 4) {
-        w[j][i] = src[i * LPR];
-      } else {
-        const uint2 p = reinterpret_cast<const uint2*>(src)[i * LPR];
-        w[j][2 * i] = p.x; w[j][2 * i + 1] = p.y;
-      }
-    }
+    for (int i = 0; i < SEGS; ++i) seg[i] = src[i * LPR];
+    __builtin_memcpy(w[j], seg, sizeof(seg));
     // a token without a slot: 0 times whatever finite codes slot 0 holds
     const float sv = c.scales[at], zv = c.zeros[at];
     s[j] = stored ? sv : 0.f;
@@ -242,15 +242,16 @@ __global__ __launch_bounds__(256) void cache_read_kernel(Cache c,
     for (int r = 0; r < 16; ++r) f[r] *= s[j];
     if (row0 + j * RPB < rows) {
       TOut* dst = (cr[j].part ? v : k) +
-                  (static_cast<uint64_t>(cr[j].t) * c.heads + cr[j].head) * N + u * 8;
-      store8<IT == 4>(dst, f);
-      store8<IT == 4>(dst + N / 2, f + 8);
+                  (static_cast<uint64_t>(cr[j].t) * c.heads + cr[j].head) * N + u * COLS;
+#pragma unroll
+      for (int i = 0; i < SEGS; ++i) store_16b<IT == 4 && LPR >= 8>(dst + i * (N / SEGS), f + i * COLS);
     }
   }
 }
 
-// More rows than this (32 MB of fp32 at 128 columns) are streamed, 4 a lane.
-constexpr uint32_t kManyRows = 65536;
+// Elements from which on rows go 4 a lane (8 heads of 128, bf16, us with one / 4 a
+// lane: 1024 tokens 3.2 / 3.8, 2048 4.2 / 3.8, 4096 6.8 / 5.1).
+constexpr uint64_t kManyElements = 1u << 22;
 
 }  // namespace
 
@@ -291,7 +292,7 @@ hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, in
       return hipGetLastError();
     };
     auto by_rows = [&](auto rot, auto* kk, auto* vv) {
-      return rows > kManyRows ? go(std::integral_constant<int, 4>{}, rot, kk, vv)
+      return static_cast<uint64_t>(rows) * N >= kManyElements ? go(std::integral_constant<int, 4>{}, rot, kk, vv)
                               : go(std::integral_constant<int, 1>{}, rot, kk, vv);
     };
     auto by_type = [&](auto rot) {

@@ -457,9 +457,8 @@ __device__ __forceinline__ void write_z(const T* __restrict__ x, const DecodeArg
 // row, each its share.
 constexpr int kEntriesEach = 8;                 // per thread: fewer rounds beat fewer registers
 constexpr int kEntries = kEntriesEach * kThreads;
-constexpr int kLocal = 16384;            // T * K of tokens transformed in LDS
+constexpr int kLocal = 4096, kLocalOne = 16384;  // T * K transformed in LDS; of one token
 constexpr int kLocalTokens = 4;
-constexpr int kLongRow = 512;            // nonzeros of a row, on average
 
 struct Entries {
   uint2 e[kEntriesEach];                            // column, value
@@ -940,11 +939,13 @@ hipError_t finish(const DecodeArgs& a, T* y, hipStream_t s) {
     return hipGetLastError();
   };
   // Rows per workgroup by what keeps the chip busy: one where there are few rows
-  // or they are long (43 rows of 8096 nonzeros: 317 us with 16 a workgroup), 8
+  // or they are longer than that (8192 columns, T = 4, whole call with one / 8 rows:
+  // 256 rows of 512 nonzeros 12.1 / 15.9 us, 1024 rows of 128, 512 and 1024
+  // 14.9 / 12.5, 16.4 / 16.4 and 18.4 / 20.7, 4096 rows of 1024 44 / 34), 8
   // up to two workgroups per compute unit, 16 beyond (4096 columns, T = 16, 128
   // nonzeros a row, whole call with 8 / 16 / 32 rows: 4096 rows 19.0 / 19.4 / 24.9
   // us, 5120 rows 23.3 / 21.1 / 25.6, 14336 rows 38.4 / 33.7 / 35.7).
-  if (a.row_ptr != nullptr && (a.N < 2048 || a.p / a.N > kLongRow))
+  if (a.row_ptr != nullptr && (a.N <= 512 || a.p / a.N > a.N - a.N / 4))
     return go(decode_finish_kernel<T, 1, true>, 1);
   if (a.N <= 4096) return go(decode_finish_kernel<T, 1, false>, 8);
   return go(decode_finish_kernel<T, 2, false>, 16);
@@ -966,10 +967,32 @@ hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   return e == hipSuccess && a.part != nullptr ? finish(a, y, s) : e;
 }
 
-// tokens few enough for the transform in LDS, rows of F short enough for one
-// workgroup's 16
+constexpr int kUnits = 256, kLds = 163840;    // compute units; LDS of one
+
+// Tiles of 16 rows a workgroup of decode_kernel takes: two where one would need
+// more workgroups than there are compute units. The compute units that get a
+// second one set the time (4096 columns, 16 tokens with one / two: 3584 rows 14.1 /
+// 15.8 us, 4000 rows 18.1 / 15.9, 28672 rows 54 / 45; one token, LOCAL, 8192 rows
+// 16.9 / 12.2). `others`: workgroups that transform tokens of 5 or more, whole
+// ones of 4096 columns; smaller ones, and those beside the lighter tiles of few
+// tokens, are over before it counts (4096 x 14336, 3 tokens 21.2 / 25.1, 8 tokens
+// 22.4 / 23.7).
+int row_tiles(int others, int N) { return others + (N + 15) / 16 > kUnits ? 2 : 1; }
+
+// Whether every workgroup transforms the tokens for itself. That saves a launch
+// and z's way through memory and costs each workgroup the transform, so: one
+// token, or several of few columns (4096 rows, 128 nonzeros a row, us with the
+// transform in LDS / through memory: 1 x 4096 9.7 / 11.1, 4 x 1024 8.9 / 9.3, 4 x
+// 4096 13.8 / 11.9); nonzeros that one round of entries holds (1 x 2048: 64 a row
+// 7.4 / 8.8, 256 11.2 / 11.1, 512 x 4 tokens 24.4 / 15.3); and all workgroups at
+// once, or two at a time on a compute unit (1 x 4096: 8192 rows 11.9 / 14.3, 9216
+// rows 21.1 / 19.5; 1 x 2048: 9216 rows 13.7 / 16.9).
 bool is_local(int T, int K, int N, int64_t p) {
-  return p > 0 && T <= kLocalTokens && T * K <= kLocal && p / N <= kLongRow;
+  if (p == 0 || T > kLocalTokens || T * K > (T == 1 ? kLocalOne : kLocal)) return false;
+  const int nt = row_tiles(0, N);
+  const int blocks = (N + 16 * nt - 1) / (16 * nt);
+  const int lds = 65536 + nt * (512 + K + 128) + T * (K + K / 16) * 4;   // steps: groups of 128
+  return 16 * nt * T * (p / N) <= kEntries && (blocks <= kUnits ? lds <= kLds : 2 * lds <= kLds);
 }
 
 template <int BITS, int MODE, typename T>
@@ -986,12 +1009,15 @@ hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   }
   if (a.tokens <= 4) {
     if (is_local(a.tokens, a.K, a.N, a.p))
-      return decode_t<BITS, MODE, 1, T, true, true>(x, a, y, s);
-    return decode_t<BITS, MODE, 1, T, true, false>(x, a, y, s);
+      return row_tiles(0, a.N) == 2 ? decode_t<BITS, MODE, 2, T, true, true>(x, a, y, s)
+                                    : decode_t<BITS, MODE, 1, T, true, true>(x, a, y, s);
+    return row_tiles(0, a.N) == 2 ? decode_t<BITS, MODE, 2, T, true, false>(x, a, y, s)
+                                  : decode_t<BITS, MODE, 1, T, true, false>(x, a, y, s);
   }
   if constexpr (sizeof(T) == 2) {
-    return a.N >= 8192 ? decode_t<BITS, MODE, 2, T, false, false>(x, a, y, s)
-                       : decode_t<BITS, MODE, 1, T, false, false>(x, a, y, s);
+    return row_tiles(a.log_b >= 12 ? a.z_blocks : 0, a.N) == 2
+               ? decode_t<BITS, MODE, 2, T, false, false>(x, a, y, s)
+               : decode_t<BITS, MODE, 1, T, false, false>(x, a, y, s);
   }
   return hipErrorInvalidValue;
 }

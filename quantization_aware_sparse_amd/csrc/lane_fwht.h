@@ -42,19 +42,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return w;
 }
 
-// 8 or 16 consecutive values as fp32 or bf16 (rounded to nearest even); STREAM:
-// past the caches, for outputs larger than they are
+// 16 bytes or 16 values, consecutive, as fp32 or bf16 (rounded to nearest even);
+// STREAM: past the caches, for outputs larger than they are
 template <bool STREAM = false, typename TOut>
-__device__ __forceinline__ void store8(TOut* dst, const float* f) {
+__device__ __forceinline__ void store_16b(TOut* dst, const float* f) {
   typedef float f32x4v __attribute__((ext_vector_type(4)));
   typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
   if constexpr (sizeof(TOut) == 4) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f32x4v* p = reinterpret_cast<f32x4v*>(dst) + i;
-      const f32x4v x = f32x4v{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-      if constexpr (STREAM) __builtin_nontemporal_store(x, p); else *p = x;
-    }
+    f32x4v* p = reinterpret_cast<f32x4v*>(dst);
+    const f32x4v x = f32x4v{f[0], f[1], f[2], f[3]};
+    if constexpr (STREAM) __builtin_nontemporal_store(x, p); else *p = x;
   } else {
     u32x4v* p = reinterpret_cast<u32x4v*>(dst);
     const u32x4v x = u32x4v{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
@@ -64,8 +61,9 @@ __device__ __forceinline__ void store8(TOut* dst, const float* f) {
 }
 template <typename TOut>
 __device__ __forceinline__ void store16(TOut* dst, const float* f) {
-  store8(dst, f);
-  store8(dst + 8, f + 8);
+  constexpr int COLS = 16 / sizeof(TOut);
+#pragma unroll
+  for (int i = 0; i < 16 / COLS; ++i) store_16b(dst + i * COLS, f + i * COLS);
 }
 
 }  // namespace qwha

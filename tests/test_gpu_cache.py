@@ -197,6 +197,16 @@ def test_read(q, T, heads, dim, page, pages, bits, rotate, act):
         assert (np.abs(got[live] - ref) <= bar).all()
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,dim,bits,rotate", [(2051, 64, 4, True), (2050, 64, 8, True),
+                                               (1027, 128, 4, False), (1031, 128, 8, True),
+                                               (515, 256, 4, True), (517, 256, 8, False)])
+def test_read_of_many_rows(q, T, dim, bits, rotate, act):
+    # four rows a lane, written past the caches where an instruction fills lines
+    assert T * 2 * 16 * dim >= 1 << 22
+    test_read(q, T, 16, dim, 16, 5, bits, rotate, act)
+
+
 @pytest.mark.parametrize("bits,rotate", [(4, True), (8, False)])
 def test_offsets_past_32_bits(q, bits, rotate):
     # more than 2^31 words of codes in each part: the last slots

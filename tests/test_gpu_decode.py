@@ -118,6 +118,21 @@ def test_layer_decode(q, T, d_out, d_in, bits, group, p, act):
     close(y, x, L, act, 0.8)
 
 
+# two tiles of rows a workgroup beside one, the largest transforms in LDS, long
+# rows of F beside few rows
+LARGE = [  # T, d_out, d_in, bits, group, p
+    (1, 4097, 8192, 4, 128, 30000), (1, 4096, 16384, 8, 128, 40000), (1, 4200, 16384, 2, 128, 900),
+    (3, 4100, 2048, 2, 32, 20000), (4, 4097, 1024, 3, 64, 9000), (2, 9000, 256, 4, 128, 5000),
+    (8, 4085, 4096, 4, 128, 7000), (16, 4000, 192, 8, 64, 9000), (4, 520, 256, 4, 64, 520 * 200),
+    (2, 500, 2048, 4, 128, 500 * 600), (1, 8193, 4096, 4, 128, 8193)]
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d_out,d_in,bits,group,p", LARGE)
+def test_layer_decode_of_many_rows(q, T, d_out, d_in, bits, group, p, act):
+    test_layer_decode(q, T, d_out, d_in, bits, group, p, act)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d_out,d_in,p", [(1, 40, 256, 3000), (3, 19, 1024, 9000),
                                             (20, 64, 128, 4000), (64, 33, 512, 8000)])
