@@ -433,12 +433,15 @@ __device__ __forceinline__ void local_transform(const T* __restrict__ x, Raw16<T
 }
 
 // zt[column][token] for z_cols columns (whole blocks) of one token: workgroup
-// `block` of the launch.
+// `block` of the launch. Workgroups go round the 8 XCDs in turn; those of one XCD
+// take neighbouring tokens, whose values lie side by side, so that its L2 joins
+// them before they go to memory.
 template <int THREADS, typename T>
 __device__ __forceinline__ void write_z(const T* __restrict__ x, const DecodeArgs& a, int block,
                                         float* lds) {
-  const int per = (a.K + a.z_cols - 1) / a.z_cols;
-  const int t = block / per, c0 = block % per * a.z_cols;
+  const int each = a.z_blocks / 8, more = a.z_blocks % 8, xcd = block % 8;
+  const int at = xcd * each + min(xcd, more) + block / 8;
+  const int t = at % a.tokens, c0 = at / a.tokens * a.z_cols;
   const int cols = min(a.z_cols, a.K - c0), items = cols >> 4;
   const T* row = x + static_cast<int64_t>(t) * a.K + c0;
   Raw16<T> raw;
