@@ -2,12 +2,13 @@
 // papernotes.org, 损失函数 / 训练策略; gist.science summary §4):
 //   y = x W_Q^T + alpha z F^T,  z = FWHT(x) / b,  T <= 64 tokens.
 //
-//   decode_kernel       up to 16 bf16 or 4 fp32 tokens: the base product on the
-//                       bf16 matrix cores, the codes read once, K split over
-//                       the waves of a workgroup; with few tokens also the
-//                       nonzeros of the same rows of F, the tokens transformed
-//                       by every workgroup for itself;
-//   decode_wide_kernel  more tokens: K split over workgroups, partial sums;
+//   decode_kernel       up to 16 bf16 or 4 fp32 tokens, more of them for layers of
+//                       fewer rows: the base product on the bf16 matrix cores,
+//                       K split over the waves of a workgroup; with few tokens
+//                       also the nonzeros of the same rows of F, the tokens
+//                       transformed by every workgroup for itself;
+//   decode_wide_kernel  more tokens, the codes read once for all of them: K split
+//                       over workgroups, partial sums;
 //   decode_finish_kernel  partial sums and the nonzeros of F added up.
 // Measured (device time; bytes that must move at the 4.9 TB/s of a copy):
 //   4096 x 4096,  4 bits, 1 token,   524288 nonzeros   8.6 us of 3.2, one launch;
@@ -551,8 +552,8 @@ __device__ __forceinline__ void nonzeros(const DecodeArgs& a, Entries& en, uint2
     for (int r = 0; r < 4; ++r) ad[w * RPW + lane / LPR][in_row * 4 + r] = s4[r];
 }
 
-// ---- up to 16 bf16 or 4 fp32 tokens
-// A workgroup takes 16 NT rows of W; its waves take the spans in turn, D of
+// ---- tiles of 16 bf16 or 4 fp32 tokens
+// A workgroup takes 16 NT rows of W and a tile of tokens; its waves take the spans in turn, D of
 // them on their way at any time, and add up their sums in LDS. The code is kept
 // short (loops, no peeled copies): a workgroup runs through much of it once, and
 // fetching instructions costs as much as fetching codes. FEW: at most 4 tokens,
@@ -585,9 +586,10 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
   }
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int n0 = (blockIdx.x - a.z_blocks) * 16 * NT;
+  const int tiles_n = (a.N + 16 * NT - 1) / (16 * NT), block = blockIdx.x - a.z_blocks;
+  const int n0 = block % tiles_n * 16 * NT, t0 = LOCAL ? 0 : block / tiles_n * TB;
   const int spans = (a.K + kSpan - 1) / kSpan;
-  const int rows = min(16 * NT, a.N - n0);
+  const int rows = min(16 * NT, a.N - n0), toks = min(a.tokens - t0, TB);
 
   int k0 = 0, kend = 0, beg = 0, end = 0;
   Raw16<T> raw;
@@ -611,7 +613,7 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
   }
 #pragma unroll
   for (int i = 0; i < PX; ++i)                          // tokens past the last repeat it
-    xoff[i] = sizeof(T) * min(4 * i + lq, a.tokens - 1) * a.K;
+    xoff[i] = sizeof(T) * (t0 + min(4 * i + lq, toks - 1)) * a.K;
 
   struct Slot {
     Code cw[NT];
@@ -693,17 +695,17 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
   }
   if constexpr (LOCAL) nonzeros<RPW, true, false>(a, en, ent, k0, kend, beg, end, 1, zl, ad);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.tokens * 16 * NT; e += kThreads) {
+  for (int e = threadIdx.x; e < toks * 16 * NT; e += kThreads) {
     const int t = e / (16 * NT), n = e % (16 * NT);
     if (n >= rows) continue;
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < kDecodeWaves; ++i) v += __uint_as_float(own[i][t * LD + n]);
     if (!LOCAL && a.part != nullptr) {
-      a.part[part_at(a, 0, t, n0 + n)] = v;
+      a.part[part_at(a, 0, t0 + t, n0 + n)] = v;
     } else {
       if constexpr (LOCAL) v = fmaf(a.alpha, ad[n][t], v);
-      Elem<T>::st(y, static_cast<int64_t>(t) * a.N + n0 + n, v);
+      Elem<T>::st(y, static_cast<int64_t>(t0 + t) * a.N + n0 + n, v);
     }
   }
 }
@@ -958,14 +960,17 @@ size_t z_lds(const DecodeArgs& a) {
   return a.z_blocks > 0 ? static_cast<size_t>(a.z_cols + a.z_cols / 16) * 4 : 0;
 }
 
+template <typename T>
+int token_tiles(int tokens) { return (tokens + Rows<T>::TOK - 1) / Rows<T>::TOK; }
+
 template <int BITS, int MODE, int NT, typename T, bool FEW, bool LOCAL>
 hipError_t decode_t(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
   const size_t staged = MODE == kWide ? static_cast<size_t>(32) * NT * (a.qw.gpr + 1) * 4 : 0;
   const size_t local = LOCAL ? static_cast<size_t>(a.tokens) * (a.K + a.K / 16) * 4 : 0;
   const size_t lds = staged + local > z_lds(a) ? staged + local : z_lds(a);
   hipLaunchKernelGGL((decode_kernel<BITS, MODE, NT, T, FEW, LOCAL>),
-                     dim3(a.z_blocks + (a.N + 16 * NT - 1) / (16 * NT)), dim3(kThreads), lds, s, x,
-                     a, y);
+                     dim3(a.z_blocks + (a.N + 16 * NT - 1) / (16 * NT) * token_tiles<T>(a.tokens)),
+                     dim3(kThreads), lds, s, x, a, y);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess && a.part != nullptr ? finish(a, y, s) : e;
 }
@@ -998,9 +1003,22 @@ bool is_local(int T, int K, int N, int64_t p) {
   return 16 * nt * T * (p / N) <= kEntries && (blocks <= kUnits ? lds <= kLds : 2 * lds <= kLds);
 }
 
+// Whether decode_wide_kernel takes the product: where decode_kernel, a workgroup
+// for every tile of tokens and two tiles of rows, and those that write z are more
+// than the compute units (17 tokens of 4096 columns without an adapter, us with
+// decode_kernel / decode_wide_kernel: 64 rows 6.0 / 8.5, 1024 rows 6.3 / 9.8, 4096
+// rows 9.4 / 15.4, 8192 rows 17.6 / 17.9, 14336 rows 31.9 / 23.2; with 64 nonzeros
+// a row and 40 tokens: 1024 rows 15.3 / 18.2, 2720 rows of 1024 columns 16.6 / 15.1,
+// 64 rows of 14336 columns 21.0 / 16.7).
+template <typename T>
+bool is_wide(int tokens, int N, int z_blocks) {
+  const int tiles = token_tiles<T>(tokens);
+  return tiles > 1 && tiles * ((N + 31) / 32) + z_blocks > kUnits;
+}
+
 template <int BITS, int MODE, typename T>
 hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
-  if (a.tokens > Rows<T>::TOK) {
+  if (is_wide<T>(a.tokens, a.N, a.z_blocks)) {
     constexpr int TB = Rows<T>::TOK * kWideTiles;
     const int blocks = (a.N + kWideRows - 1) / kWideRows * ((a.tokens + TB - 1) / TB) * a.slices;
     const size_t tiles = sizeof(uint32_t) * 2 * kWideTiles * kTileWords +
@@ -1017,12 +1035,10 @@ hipError_t decode_m(const T* x, const DecodeArgs& a, T* y, hipStream_t s) {
     return row_tiles(0, a.N) == 2 ? decode_t<BITS, MODE, 2, T, true, false>(x, a, y, s)
                                   : decode_t<BITS, MODE, 1, T, true, false>(x, a, y, s);
   }
-  if constexpr (sizeof(T) == 2) {
-    return row_tiles(a.log_b >= 12 ? a.z_blocks : 0, a.N) == 2
-               ? decode_t<BITS, MODE, 2, T, false, false>(x, a, y, s)
-               : decode_t<BITS, MODE, 1, T, false, false>(x, a, y, s);
-  }
-  return hipErrorInvalidValue;
+  constexpr bool FEW = sizeof(T) == 4;       // tiles of 4 fp32 tokens
+  return row_tiles(a.log_b >= 12 ? a.z_blocks : 0, a.N * token_tiles<T>(a.tokens)) == 2
+             ? decode_t<BITS, MODE, 2, T, FEW, false>(x, a, y, s)
+             : decode_t<BITS, MODE, 1, T, FEW, false>(x, a, y, s);
 }
 
 template <int BITS, typename T>
@@ -1063,8 +1079,8 @@ int wide_slices(int z_blocks, int K, int N) {
 struct DecodeWs {
   size_t part, total;     // zt at 0
 };
-// Calls of both types find room: fp32 ones take decode_wide_kernel from 5 tokens
-// on, bf16 ones from 17.
+// Calls of both types find room: fp32 ones may take decode_wide_kernel from 5
+// tokens on, bf16 ones from 17.
 DecodeWs decode_ws(int T, int K, int N, int64_t p) {
   DecodeWs l;
   const bool z = p > 0 && !is_local(T, K, N, p);
@@ -1091,18 +1107,19 @@ hipError_t launch_decode(const void* x, Dt dt, int T, int log_n, int nblk, int N
   a.E = E;
   a.c = c;
   a.log_b = log_n;
-  const bool wide = T > (dt == Dt::F32 ? Rows<float>::TOK : Rows<uint16_t>::TOK);
   const bool through_memory = p > 0 && !is_local(T, a.K, N, p);
   a.p = p;
+  // whole blocks of columns, 2048 together at least, in one workgroup
+  a.z_cols = log_n >= 11 ? 1 << log_n : 2048;
+  a.z_blocks = through_memory ? T * ((a.K + a.z_cols - 1) / a.z_cols) : 0;
+  const bool wide = dt == Dt::F32 ? is_wide<float>(T, N, a.z_blocks)
+                                  : is_wide<uint16_t>(T, N, a.z_blocks);
   a.part = wide || through_memory
                ? reinterpret_cast<float*>(static_cast<char*>(scratch) + decode_ws(T, a.K, N, p).part)
                : nullptr;
   a.slices = wide ? wide_slices(through_memory ? T : 0, a.K, N) : 1;
   a.z_out = static_cast<float*>(scratch);
   a.zt = a.z_out;
-  // whole blocks of columns, 2048 together at least, in one workgroup
-  a.z_cols = log_n >= 11 ? 1 << log_n : 2048;
-  a.z_blocks = through_memory ? T * ((a.K + a.z_cols - 1) / a.z_cols) : 0;
   a.alpha = through_memory ? alpha : alpha / static_cast<float>(1 << log_n);
   if (dt == Dt::F32) return decode_d(static_cast<const float*>(x), a, static_cast<float*>(y), s);
   return decode_d(static_cast<const uint16_t*>(x), a, static_cast<uint16_t*>(y), s);

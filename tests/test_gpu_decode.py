@@ -133,6 +133,19 @@ def test_layer_decode_of_many_rows(q, T, d_out, d_in, bits, group, p, act):
     test_layer_decode(q, T, d_out, d_in, bits, group, p, act)
 
 
+# many tokens of many rows: K split over workgroups
+WIDE = [  # T, d_out, d_in, bits, group, p
+    (64, 2100, 320, 4, 64, 9000), (33, 2751, 192, 8, 32, 20000), (17, 4130, 128, 3, 64, 0),
+    (64, 2065, 1024, 2, 128, 30000), (40, 2750, 4096, 4, 128, 8000), (64, 2049, 64, 4, 32, 5000),
+    (63, 1600, 16384, 3, 32, 4000), (50, 2800, 960, 8, 64, 0), (18, 4100, 448, 2, 32, 5000)]
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d_out,d_in,bits,group,p", WIDE)
+def test_layer_decode_of_many_tokens(q, T, d_out, d_in, bits, group, p, act):
+    test_layer_decode(q, T, d_out, d_in, bits, group, p, act)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d_out,d_in,p", [(1, 40, 256, 3000), (3, 19, 1024, 9000),
                                             (20, 64, 128, 4000), (64, 33, 512, 8000)])
