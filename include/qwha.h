@@ -406,7 +406,7 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
  * tokens (QWHA_ERR_SHAPE beyond: qwha_layer_fwd's tiles are the better fit
  * there). Weights, adapter and widths as qwha_layer_fwd (d_in >= 64, group >=
  * 32); x [T][d_in] and y [T][d_out] share `act`, QWHA_BF16 or QWHA_F32. The
- * codes are read once for all tokens. Sums are fp32; fp32 x enters with its
+ * codes come from memory once a call. Sums are fp32; fp32 x enters with its
  * 24 bits, a bf16 y is rounded once. p = 0 is the base layer alone (row_ptr, E
  * and c are then not read and may be NULL). Workspace:
  * qwha_layer_decode_workspace_bytes(T, d_in, d_out, p) bytes (0 when out of
