@@ -28,15 +28,19 @@ __device__ __forceinline__ float row_extreme(float m) {
 }
 
 // floor(v / s + 1/2) + add exactly, for |v| up to about 2^8 s. The quotient
-// from the reciprocal is off by less than 2^-14, so floor(v/s + 1/2 - 2^-12) is
-// the result or, beside a border, one below it; the residual r = v - q s then
-// decides, and one fma gives it exactly: where |v| >= s both v and q s are
-// multiples of ulp(s) and r is at most s; below, q is 0 or -1 and r is v or the
-// exact difference of two numbers within a factor of two. So the code is what
+// from the reciprocal is off by less than 2^-14, so q = floor(v/s + 1/2 - 2^-12)
+// is the result or, beside a border, one below it; the residual r = v - q s, in
+// [-s/2, s], then decides. One fma gives it: where |v| >= s both v and q s are
+// multiples of ulp(s) and r is at most s, so it is exact; below, q is -1, 0 or 1
+// and r is v, or v less or plus s, exact within a factor of two of each other and
+// else on the side of s/2 that the exact difference is on, which rounding does
+// not leave. The residual is doubled (exact) and not the step halved: half a step
+// below 2^-125 may need a bit below fp32's smallest number. So the code is what
 // infinite precision gives for this v and s, whatever computes it.
-__device__ __forceinline__ int round_half_up(float v, float s, float half, float inv, int add) {
+__device__ __forceinline__ int round_half_up(float v, float s, float inv, int add) {
   const float q = floorf(fmaf(v, inv, 0.5f - 0x1p-12f));
-  return static_cast<int>(q) + add + (fmaf(-q, s, v) >= half ? 1 : 0);
+  const float r = fmaf(-q, s, v);
+  return static_cast<int>(q) + add + (r + r >= s ? 1 : 0);
 }
 
 // Row `row` of a call's [T][2][heads] rows: keys, then values, head by head.
@@ -99,14 +103,14 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict_
   float s = (hi - lo) / QMAX;
   const bool flat = !(s >= 1.17549435e-38f);   // a step below fp32's normal range holds nothing
   if (flat) s = 0.f;
-  const float inv = flat ? 0.f : 1.f / s, half = 0.5f * s;
-  const int z = flat ? 0 : round_half_up(-lo, s, half, inv, 0);
+  const float inv = flat ? 0.f : 1.f / s;
+  const int z = flat ? 0 : round_half_up(-lo, s, inv, 0);
   uint32_t w[WORDS];
 #pragma unroll
   for (int i = 0; i < WORDS; ++i) w[i] = 0u;
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
-    const int q = min(max(round_half_up(f[r], s, half, inv, z), 0), (1 << BITS) - 1);
+    const int q = min(max(round_half_up(f[r], s, inv, z), 0), (1 << BITS) - 1);
     w[r * BITS / 32] |= static_cast<uint32_t>(q) << (r * BITS % 32);
   }
   if (row >= rows || slot < 0 || (slot >> c.lg_page) >= c.n_pages) return;
