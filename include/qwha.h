@@ -441,7 +441,10 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *     lo = min(v, 0), hi = max(v, 0), s = fp32(fp32(hi - lo) / (2^b - 1)),
  *     z = floor(-lo / s + 1/2), q = clip(floor(v / s + 1/2) + z, 0, 2^b - 1),
  *   the transform in fp64 and both floors as exact arithmetic on the fp32 v
- *   and s gives them. A step below 2^-126 stores s = z = q = 0. A slot outside
+ *   and s gives them. A step below 2^-126 stores s = z = q = 0; a row that holds
+ *   a NaN or an infinity, or whose fp32(hi - lo) is infinite (with `rotate` it is
+ *   finite where x is, as |v| and hi - lo are at most the largest |x|), stores
+ *   s = NaN, z = q = 0, and reads back as NaN. A slot outside
  *   [0, n_pages * page) is skipped (padding). The slots of one call that are
  *   not skipped must be distinct (not checked; two tokens on one slot leave a
  *   mixture of both there and touch nothing else).
@@ -462,8 +465,7 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   bytes (0 when out of range), 256-byte aligned; calls that may overlap
  *   need one each.
  * Values read (k, v, q, and the cache's rows in use) must be finite, as for
- * every call here, and so must fp32(hi - lo) (with `rotate` it is, as |v| and
- * hi - lo are at most the largest |x|); others spoil their own rows only. Out-of-range slots and
+ * every call here; others spoil their own rows only. Out-of-range slots and
  * pages are checked on the device and never read or written through.
  * --------------------------------------------------------------------------- */
 qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64_t T,

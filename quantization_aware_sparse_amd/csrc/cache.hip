@@ -8,7 +8,8 @@
 // row suffice. v is quantized to b bits over its range with zero included:
 //   lo = min(v, 0), hi = max(v, 0), s = fp32(fp32(hi - lo) / (2^b - 1)),
 //   z = floor(-lo/s + 1/2), q = clip(floor(v/s + 1/2) + z, 0, 2^b - 1),
-// and read back as x' = s (q - z) H.
+// and read back as x' = s (q - z) H. A row that is not finite gets s = NaN and
+// z = q = 0, so that whatever uses it shows it.
 #include "cache.h"
 #include "lane_fwht.h"
 
@@ -24,6 +25,15 @@ __device__ __forceinline__ float row_extreme(float m) {
   if constexpr (LANES > 2) m = pick(m, lane_xor<2>(m));
   if constexpr (LANES > 4) m = pick(m, lane_xor<4>(m));
   if constexpr (LANES > 8) m = pick(m, lane_xor<8>(m));
+  return m;
+}
+
+template <int LANES>
+__device__ __forceinline__ float row_sum(float m) {
+  if constexpr (LANES > 1) m += lane_xor<1>(m);
+  if constexpr (LANES > 2) m += lane_xor<2>(m);
+  if constexpr (LANES > 4) m += lane_xor<4>(m);
+  if constexpr (LANES > 8) m += lane_xor<8>(m);
   return m;
 }
 
@@ -98,11 +108,21 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict_
     lo = fminf(lo, f[r]);
     hi = fmaxf(hi, f[r]);
   }
+  // NaN, which the extremes pass over, where a value is not finite (0 * f). The
+  // transform adds every value of the row to each of its results: any one tells.
+  float bad = 0.f * f[0];
+  if constexpr (!ROT) {
+#pragma unroll
+    for (int r = 1; r < PER; ++r) bad = fmaf(0.f, f[r], bad);
+    bad = row_sum<LPR>(bad);
+  }
   lo = row_extreme<LPR, false>(lo);
   hi = row_extreme<LPR, true>(hi);
   float s = (hi - lo) / QMAX;
-  const bool flat = !(s >= 1.17549435e-38f);   // a step below fp32's normal range holds nothing
-  if (flat) s = 0.f;
+  const bool lost = !(s + bad < INFINITY);     // not finite, or a range past fp32's
+  // a step below fp32's normal range holds nothing
+  const bool flat = lost || !(s >= 1.17549435e-38f);
+  if (flat) s = lost ? __builtin_nanf("") : 0.f;
   const float inv = flat ? 0.f : 1.f / s;
   const int z = flat ? 0 : round_half_up(-lo, s, inv, 0);
   uint32_t w[WORDS];
