@@ -459,13 +459,17 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   [B]. Sums and the softmax are fp32, fp32 queries enter with their 24 bits.
  *   lens[b] <= 0 gives a row of zeros, lens[b] above width * page counts as
  *   width * page, and the tokens of a table entry outside [0, n_pages) are
- *   left out. Nothing at or behind lens[b] is used, whatever it holds.
+ *   left out. Nothing at or behind lens[b] is used, whatever it holds. A NaN or
+ *   an infinity in a row of q, or in the step or zero of a key or value that it
+ *   is attended with, gives a row of out that holds no finite number (NaN, or for
+ *   values an infinity). A score above fp32's range gives NaN, one below it
+ *   weighs nothing, and a row all of whose scores lie below it is zeros.
  *   Requires heads to divide q_heads, 0 <= B <= 65535. Workspace:
  *   qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
  *   bytes (0 when out of range), 256-byte aligned; calls that may overlap
  *   need one each.
- * Values read (k, v, q, and the cache's rows in use) must be finite, as for
- * every call here; others spoil their own rows only. Out-of-range slots and
+ * Values read (k, v, q, and the cache's rows in use) should be finite; others
+ * spoil the rows said above and no more. Out-of-range slots and
  * pages are checked on the device and never read or written through.
  * --------------------------------------------------------------------------- */
 qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64_t T,

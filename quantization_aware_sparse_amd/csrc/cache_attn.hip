@@ -30,6 +30,11 @@
 // 8 bits 23.1 + 4.1 us of 21; one of 777, 8 x 4 heads of 128 5.8 + 3.8 us of 0.2.
 //
 // cache_combine_kernel joins the slices: one maximum, one sum, one transform.
+//
+// A row without tokens is known by a sum of exactly 0. What is not finite is
+// passed on: a NaN score is in the sums though not in the maximum, +inf makes
+// its own weight NaN; -inf, from finite rows whose product passes fp32's range,
+// weighs nothing.
 #include <algorithm>
 
 #include "cache.h"
@@ -68,6 +73,12 @@ __device__ __forceinline__ float quarter_max(float v) {
   v = fmaxf(v, lane_xor<2>(v));
   v = fmaxf(v, lane_xor<4>(v));
   return fmaxf(v, lane_xor<8>(v));
+}
+__device__ __forceinline__ uint32_t quarter_max(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(lane_xor_i32<1>(static_cast<int>(v))));
+  v = max(v, static_cast<uint32_t>(lane_xor_i32<2>(static_cast<int>(v))));
+  v = max(v, static_cast<uint32_t>(lane_xor_i32<4>(static_cast<int>(v))));
+  return max(v, static_cast<uint32_t>(lane_xor_i32<8>(static_cast<int>(v))));
 }
 __device__ __forceinline__ float quarter_sum(float v) {
   v += lane_xor<1>(v);
@@ -193,20 +204,23 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
   float qunit[HT], qsum[HT];                        // of head lq: 2^(e - 23), sum of Q
 #pragma unroll
   for (int t = 0; t < HT; ++t) {
+    // as bits, in which infinities and NaN are above all numbers
     auto largest = [&](int head) {
-      float top = 0.f;
+      uint32_t top = 0u;
 #pragma unroll
-      for (int i = 0; i < J; ++i) top = fmaxf(top, fabsf(qs[head][lr * J + i]));
+      for (int i = 0; i < J; ++i) top = max(top, __float_as_uint(fabsf(qs[head][lr * J + i])));
       return quarter_max(top);
     };
     // the maximum of head t * 4 + lq is at hand in quarter lq, that of the
     // lane's row, head lr / 4, in quarter lr / 4
-    const float top = largest(t * 4 + lq);
+    const uint32_t top = largest(t * 4 + lq);
+    const int finite = top < 0x7F800000u;
     int e = 0;
-    if (frexpf(top, &e) > 0.99f) ++e;
+    if (frexpf(finite ? __uint_as_float(top) : 0.f, &e) > 0.99f) ++e;
     e = max(e, -100);
-    qunit[t] = ldexpf(1.f, e - 23);
+    qunit[t] = finite ? ldexpf(1.f, e - 23) : __builtin_nanf("");   // makes every score NaN
     const float unit = ldexpf(1.f, 23 - __shfl(e, (lr >> 2) * 16));
+    const int whole = __shfl(finite, (lr >> 2) * 16);
     float sum = 0.f;
     const float inv = ldexpf(1.f, 23 - e);
 #pragma unroll
@@ -222,8 +236,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
           // column of byte i of register r: 4-bit words give their even codes
           // first, then their odd ones
           const int at = BITS == 4 ? r / 2 * 8 + 2 * i + r % 2 : r * 4 + i;
-          const int v = static_cast<int>(
-              rintf(qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 16 + at] * unit));
+          const float f = rintf(qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 16 + at] * unit);
+          const int v = whole ? static_cast<int>(f) : 0;
           const int d2 = static_cast<int8_t>(v), v1 = (v - d2) >> 8;
           const int d1 = static_cast<int8_t>(v1), d0 = (v1 - d1) >> 8;
           const int d = (lr & 3) == 0 ? d0 : (lr & 3) == 1 ? d1 : d2;
@@ -337,9 +351,12 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
           sg[t][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qf[t][s], kf, s ? sg[t][i] : izero4, 0, 0, 0);
       }
     // what lies in a place that is left out is never used, whatever it holds
-    float sv[2], ov[2];
+    float sv[2], ov[2], lost[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      // 0, or NaN where a key's step or zero is not finite: its score is then NaN,
+      // and not an infinity that might weigh nothing
+      lost[i] = fmaf(0.f, cur.sk[i], 0.f * cur.zk[i]);
       sv[i] = cur.live[i] ? cur.sv[i] : 0.f;
       ov[i] = cur.live[i] ? OFF + cur.zv[i] : 0.f;
     }
@@ -351,7 +368,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
         const float d = fmaf(65536.f, static_cast<float>(sg[t][i][0]),
                              fmaf(256.f, static_cast<float>(sg[t][i][1]),
                                   static_cast<float>(sg[t][i][2])));
-        const float x = cur.sk[i] * qunit[t] * fmaf(KOFF - cur.zk[i], qsum[t], d);
+        const float x =
+            fmaf(cur.sk[i] * qunit[t], fmaf(KOFF - cur.zk[i], qsum[t], d), lost[i]);
         s[i] = cur.live[i] ? x : -INFINITY;
       }
       const float mn = fmaxf(m[t], quarter_max(fmaxf(s[0], s[1])));
@@ -431,21 +449,21 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wml[i][head].x);
+    // a NaN score is passed over by the maximum and stays in the sums
+    const float at = top == -INFINITY ? 0.f : top;
     float o = 0.f, sum = 0.f;
-    if (top > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < WAVES; ++i) {
-        const float f = exp2_fast(wml[i][head].x - top);
-        o = fmaf(f, om[i][head][d], o);
-        sum = fmaf(f, wml[i][head].y, sum);
-      }
+    for (int i = 0; i < WAVES; ++i) {
+      const float f = exp2_fast(wml[i][head].x - at);
+      o = fmaf(f, om[i][head][d], o);
+      sum = fmaf(f, wml[i][head].y, sum);
     }
     if (a.slices == 1) {
-      qs[head][d] = sum > 0.f ? o / sum : 0.f;
+      qs[head][d] = sum == 0.f ? 0.f : o / sum;     // no tokens
     } else {
-      const int64_t at = (qrow + head) * a.slices + slice;
-      a.part[at * N + d] = o;
-      if (d == 0) a.ml[at] = float2{top, sum};
+      const int64_t row = (qrow + head) * a.slices + slice;
+      a.part[row * N + d] = o;
+      if (d == 0) a.ml[row] = float2{top, sum};
     }
   }
   if (a.slices == 1) {
@@ -475,7 +493,7 @@ __global__ __launch_bounds__(kAttnThreads) void cache_combine_kernel(AttnArgs a,
     float4 o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = p[i];
-    if (!(x.y > 0.f)) continue;                    // a slice without tokens: nothing written
+    if (x.y == 0.f) continue;                      // a slice without tokens; NaN goes on
     const float mn = fmaxf(top, x.x), keep = exp2_fast(top - mn), f = exp2_fast(x.x - mn);
     top = mn;
     sum = fmaf(f, x.y, sum * keep);
@@ -495,15 +513,14 @@ __global__ __launch_bounds__(kAttnThreads) void cache_combine_kernel(AttnArgs a,
   if (tid < N) {
     top = -INFINITY;
     for (int i = 0; i < used; ++i) top = fmaxf(top, gml[i].x);
+    const float at = top == -INFINITY ? 0.f : top;
     float o = 0.f, l = 0.f;
-    if (top > -INFINITY) {
-      for (int i = 0; i < used; ++i) {
-        const float f = exp2_fast(gml[i].x - top);
-        o = fmaf(f, os[i][tid], o);
-        l = fmaf(f, gml[i].y, l);
-      }
+    for (int i = 0; i < used; ++i) {
+      const float f = exp2_fast(gml[i].x - at);
+      o = fmaf(f, os[i][tid], o);
+      l = fmaf(f, gml[i].y, l);
     }
-    os[0][tid] = l > 0.f ? o / l : 0.f;            // column tid is this thread's alone
+    os[0][tid] = l == 0.f ? 0.f : o / l;           // column tid is this thread's alone
   }
   __syncthreads();
   if (tid < J) finish_row<N>(os[0], u, a.rotate, out + row * N);
