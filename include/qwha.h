@@ -456,7 +456,9 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   k_t and v_t the rows read back (without being written out) of key/value
  *   head i / (q_heads / heads) in page table[b][t / page] at t % page; q and
  *   out [B][q_heads][head_dim] in `act`, table int32 [B][width], lens int32
- *   [B]. Sums and the softmax are fp32, fp32 queries enter with their 24 bits.
+ *   [B]. Sums and the softmax are fp32. q' = scale log2(e) q (times H with
+ *   rotate), formed in fp32, enters with 32 bits counted from its head's largest
+ *   component: each is off by 1.02 * 2^-31 of that one at most.
  *   lens[b] <= 0 gives a row of zeros, lens[b] above width * page counts as
  *   width * page, and the tokens of a table entry outside [0, n_pages) are
  *   left out. Nothing at or behind lens[b] is used, whatever it holds. A NaN or

@@ -8,21 +8,25 @@
 // heads that read it, and a slice of the tokens; its waves take tiles of 32
 // tokens in turn, each with its own running maximum and sum of the softmax.
 //   scores  on the 8-bit integer matrix cores (v_mfma_i32_16x16x64_i8), exact.
-//           A: 16 rows = 4 query heads x (upper, middle, lower digit, unused):
-//           q' as a 24-bit fixed-point number of the head's own power of two, in
-//           three signed digits of 8 bits; B: 16 tokens' codes (8-bit ones less
-//           128). Codes need a mask and a shift to be operands, as bf16 a
-//           permutation and an or of each pair as well. Lane l holds token
-//           l % 16 and a quarter of its row;
+//           A: 16 rows = 4 query heads x 4 signed digits of 8 bits: q' is rounded
+//           to a whole number of 2^(e - 31), 2^e the power of two above the head's
+//           largest |q'|. That keeps all 24 bits of components of 2^-6 of the
+//           largest and more, and leaves the others an error of 1.02 * 2^-31 of it
+//           at most, 1/128 of what one rounding of an fp32 sum with the largest in
+//           it costs. B: 16 tokens' codes (8-bit ones less 128). Codes need a mask
+//           and a shift to be operands, as bf16 a permutation and an or of each
+//           pair as well. Lane l holds token l % 16 and a quarter of its row;
 //   values  on the bf16 matrix cores (v_mfma_f32_16x16x32_bf16). A: the weights
 //           p s_v as three bf16 numbers that sum to them exactly; B: for each of
 //           N / 16 columns j the codes of column (N / 16) (l % 16) + j of 8
 //           tokens: a lane reads its N / 16 columns of 8 tokens and pairs the
 //           tokens' codes up, as 16 + q (4 bits) or q (8 bits), exact in bf16.
 // What is constant in (q - z) is taken off in fp32:
-//   score   = s_k (sum q' code' + (0 or 128 - z_k) sum q'),
+//   score   = s_k sum_i 256^(3-i) (sum d_i code' + (0 or 128 - z_k) sum d_i), digit
+//             sums d_i by digit sums: whole numbers below 2^24 for whole z_k, so a
+//             column whose code is its zero point leaves nothing, however large q';
 //   output  = sum p s_v (OFF + code) - sum p s_v (OFF + z_v).
-// A head's three parts lie in one lane's results.
+// A head's parts lie in one lane's results.
 // Bound by the vector units, which unpack: about 250 instructions of a wave for
 // 32 tokens of 128 columns, 9 KB of 4-bit keys and values. Measured (device time;
 // the cache's bytes at the 4.9 TB/s of a copy): 32 sequences of 1900 .. 4096 tokens,
@@ -196,12 +200,16 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
   __syncthreads();
 
   const PartMask pm(lr & 3);
-  // digits of the queries: q' = 2^(e - 23) Q with 0.99 * 2^e above the head's
-  // largest |q'|, so that Q = (d0 256 + d1) 256 + d2 in digits of -128 .. 127.
+  const uint32_t pick = 0x0703u - 0x0101u * (lr & 3);   // the lane's digit of two numbers
+  // digits of the queries: q' = 2^(e - 31) Q with 0.99 * 2^e above the head's
+  // largest |q'|, so that Q = ((d0 256 + d1) 256 + d2) 256 + d3 in digits of
+  // -128 .. 127.
   // Lane l: row l % 16 = (head, digit), the columns of its quarter in the order
   // of the codes' operands.
   i32x4 qf[HT][STEPS];
-  float qunit[HT], qsum[HT];                        // of head lq: 2^(e - 23), sum of Q
+  int qexp[HT];                                     // of head lq: e - 31,
+  float dsum[HT][3];                                // sums of d0, d1 and d2 256 + d3
+  const i32x4 izero4 = i32x4{0, 0, 0, 0};
 #pragma unroll
   for (int t = 0; t < HT; ++t) {
     // as bits, in which infinities and NaN are above all numbers
@@ -215,41 +223,44 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
     // lane's row, head lr / 4, in quarter lr / 4
     const uint32_t top = largest(t * 4 + lq);
     const int finite = top < 0x7F800000u;
-    int e = 0;
-    if (frexpf(finite ? __uint_as_float(top) : 0.f, &e) > 0.99f) ++e;
-    e = max(e, -100);
-    qunit[t] = finite ? ldexpf(1.f, e - 23) : __builtin_nanf("");   // makes every score NaN
-    const float unit = ldexpf(1.f, 23 - __shfl(e, (lr >> 2) * 16));
-    const int whole = __shfl(finite, (lr >> 2) * 16);
-    float sum = 0.f;
-    const float inv = ldexpf(1.f, 23 - e);
-#pragma unroll
-    for (int i = 0; i < J; ++i) sum += rintf(qs[t * 4 + lq][lr * J + i] * inv);
-    qsum[t] = quarter_sum(sum);
+    const float largest_q = finite ? __uint_as_float(top) : 0.f;
+    const int e = __builtin_amdgcn_frexp_expf(largest_q) +
+                  (__builtin_amdgcn_frexp_mantf(largest_q) > 0.99f ? 1 : 0);
+    qexp[t] = e - 31;
+    const int up = 31 - __shfl(e, (lr >> 2) * 16), whole = __shfl(finite, (lr >> 2) * 16);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        uint32_t x = 0u;
+        uint32_t b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // column of byte i of register r: 4-bit words give their even codes
           // first, then their odd ones
           const int at = BITS == 4 ? r / 2 * 8 + 2 * i + r % 2 : r * 4 + i;
-          const float f = rintf(qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 16 + at] * unit);
-          const int v = whole ? static_cast<int>(f) : 0;
-          const int d2 = static_cast<int8_t>(v), v1 = (v - d2) >> 8;
-          const int d1 = static_cast<int8_t>(v1), d0 = (v1 - d1) >> 8;
-          const int d = (lr & 3) == 0 ? d0 : (lr & 3) == 1 ? d1 : d2;
-          x |= static_cast<uint32_t>(d & 0xFF) << (8 * i);
+          const float f = rintf(__builtin_amdgcn_ldexpf(
+              qs[t * 4 + (lr >> 2)][lq * (N / 4) + s * 16 + at], up));
+          // Q + 128 (256^3 + 256^2 + 256 + 1) has the digits, each with 128 added
+          b[i] = static_cast<uint32_t>(whole ? static_cast<int>(f) : 0) + 0x80808080u;
         }
+        const uint32_t x = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], pick),
+                                                 __builtin_amdgcn_perm(b[1], b[0], pick),
+                                                 0x05040100u) ^ 0x80808080u;
         qf[t][s][r] = static_cast<int>(x);
       }
+    const i32x4 iones4 = i32x4{0x01010101, 0x01010101, 0x01010101, 0x01010101};
+    i32x4 ds = izero4;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+      ds = __builtin_amdgcn_mfma_i32_16x16x64_i8(qf[t][s], iones4, ds, 0, 0, 0);
+    dsum[t][0] = static_cast<float>(ds[0]);
+    dsum[t][1] = static_cast<float>(ds[1]);
+    // NaN makes every score of the head NaN
+    dsum[t][2] = finite ? static_cast<float>(ds[2] * 256 + ds[3]) : __builtin_nanf("");
   }
 
   const uint32_t mask = in_vgpr(kMask4);
   const f32x4 zero4 = f32x4{0.f, 0.f, 0.f, 0.f};
-  const i32x4 izero4 = i32x4{0, 0, 0, 0};
   const int64_t vals = c.part_rows();
   const uint32_t in_page = (1u << c.lg_page) - 1;
   f32x4 acc[HT][J];
@@ -365,11 +376,16 @@ __global__ __launch_bounds__(WAVES * 64, 2) void cache_attn_kernel(const T* __re
       float s[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float d = fmaf(65536.f, static_cast<float>(sg[t][i][0]),
-                             fmaf(256.f, static_cast<float>(sg[t][i][1]),
-                                  static_cast<float>(sg[t][i][2])));
-        const float x =
-            fmaf(cur.sk[i] * qunit[t], fmaf(KOFF - cur.zk[i], qsum[t], d), lost[i]);
+        // the lower two digits together, below 2^31: their rounding to fp32 is less
+        // than what rounding q' to whole numbers costs
+        const float z = KOFF - cur.zk[i];
+        const float d0 = fmaf(z, dsum[t][0], static_cast<float>(sg[t][i][0]));
+        const float d1 = fmaf(z, dsum[t][1], static_cast<float>(sg[t][i][1]));
+        const float d2 = fmaf(z, dsum[t][2], static_cast<float>(sg[t][i][2] * 256 + sg[t][i][3]));
+        // the step takes the power of two: where that passes below fp32's range the
+        // score is 0 to within 2^-100
+        const float x = fmaf(__builtin_amdgcn_ldexpf(cur.sk[i], qexp[t]),
+                             fmaf(0x1p24f, d0, fmaf(0x1p16f, d1, d2)), lost[i]);
         s[i] = cur.live[i] ? x : -INFINITY;
       }
       const float mn = fmaxf(m[t], quarter_max(fmaxf(s[0], s[1])));
