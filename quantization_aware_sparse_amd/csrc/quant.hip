@@ -363,9 +363,11 @@ __device__ __forceinline__ bf16x8 unpack_off128(uint32_t w, uint32_t mask) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t x = __builtin_amdgcn_perm(u, w, 0x0C040C00u + 0x00010001u * i);
-    // (x & mask) | 0x43004300 in one instruction (mask 0x000F000F in a VGPR:
-    // one scalar operand per VALU instruction on this target)
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(d[i]) : "v"(x), "v"(mask), "s"(0x43004300u));
+    // one v_and_or_b32 (mask 0x000F000F in a VGPR: one scalar operand per VALU
+    // instruction on this target). Left to the compiler, which puts the two wait
+    // states between it and a matrix instruction that reads its result; around
+    // inline asm it puts none.
+    d[i] = (x & mask) | 0x43004300u;
   }
   bf16x8 r;
   __builtin_memcpy(&r, d, 16);
