@@ -16,10 +16,6 @@ from typing import Dict, Optional
 import torch
 
 from ._lib import QwhaError, check, lib  # noqa: F401
-from . import _binding
-
-_binding.set_error(QwhaError)
-
 __all__ = [
     "QWHA_F32", "QWHA_BF16", "QwhaError", "lib",
     "QWHA_SELECT_MAGNITUDE", "QWHA_SELECT_RANDOM",
@@ -210,6 +206,29 @@ def qwha_layer_fwd(x: torch.Tensor, codes, scales, zeros, bits: int, group: int,
 
 
 # ---------------------------------------------------------------- decoding
+class _Decoding:
+    """Stands for the compiled binding until the first decoding call: the rest of
+    the package does not need it."""
+
+    def __getattr__(self, name):
+        import importlib
+        global _decoding
+        if name.startswith("__"):
+            raise AttributeError(name)
+        try:
+            loaded = importlib.import_module("._binding", __name__)
+        except ImportError as e:
+            raise ImportError("the decoding calls' compiled binding is not built for this Python "
+                              "and torch; run `python quantization_aware_sparse_amd/build.py` "
+                              f"({e})") from e
+        loaded.set_error(QwhaError)
+        _decoding = loaded       # later calls find it here
+        return getattr(loaded, name)
+
+
+_decoding = _Decoding()
+
+
 # These calls are short, and Python's share of them would be the larger part: the
 # checks of types, shapes and devices, the outputs, the workspace and the stream
 # (the current one of the tensors' device, which need not be the current device)
@@ -221,7 +240,7 @@ def qwha_layer_decode(x: torch.Tensor, codes, scales, zeros, bits: int, group: i
     """qwha_layer_fwd for the few tokens of a decoding step: y = x W_Q^T + alpha
     z F^T for x [T][d_in], T <= QWHA_DECODE_MAX_T, bf16 or fp32 (y alike).
     Without an adapter (c None or empty) the base layer alone."""
-    return _binding.layer_decode(x, codes, scales, zeros, bits, group, row_ptr, E, c, alpha, y, ws)
+    return _decoding.layer_decode(x, codes, scales, zeros, bits, group, row_ptr, E, c, alpha, y, ws)
 
 
 def qwha_cache_empty(n_pages: int, heads: int, page: int, head_dim: int, bits: int, device):
@@ -240,7 +259,7 @@ def qwha_cache_write(k: torch.Tensor, v: torch.Tensor, slots, codes, scales, zer
     (int32 [T], page * page_size + offset; others, as -1, are skipped) of a
     cache made by qwha_cache_empty; with rotate through the Walsh-Hadamard
     transform of each row."""
-    _binding.cache_write(k, v, slots, codes, scales, zeros, bits, rotate)
+    _decoding.cache_write(k, v, slots, codes, scales, zeros, bits, rotate)
 
 
 def qwha_cache_read(codes, scales, zeros, slots, bits: int, head_dim: int, rotate: bool = True,
@@ -251,7 +270,7 @@ def qwha_cache_read(codes, scales, zeros, slots, bits: int, head_dim: int, rotat
     it."""
     if out_dtype not in _DT:
         raise TypeError(f"unsupported dtype {out_dtype}")
-    return _binding.cache_read(codes, scales, zeros, slots, bits, head_dim, rotate,
+    return _decoding.cache_read(codes, scales, zeros, slots, bits, head_dim, rotate,
                                _DT[out_dtype] == QWHA_F32, k, v)
 
 
@@ -263,7 +282,7 @@ def qwha_cache_attn(q: torch.Tensor, codes, scales, zeros, table, lens, bits: in
     or bf16, the output alike), over the first lens[b] tokens of the pages
     table[b] (int32 [B] and [B][width]) of a cache; scale 1/sqrt(head_dim)
     unless given."""
-    return _binding.cache_attn(q, codes, scales, zeros, table, lens, bits, rotate, scale, out, ws)
+    return _decoding.cache_attn(q, codes, scales, zeros, table, lens, bits, rotate, scale, out, ws)
 
 
 # ---------------------------------------------------------------- materialize
