@@ -432,7 +432,8 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *          row in word j / cpw at bit (j % cpw) * bits, cpw = 32 / bits;
  *   scales, zeros  fp32 [2][n_pages][heads][page].
  * bits is 4 or 8, head_dim 64, 128 or 256, page a power of two in [8, 1024],
- * n_pages * page <= 2^31 - 1. Token position `off` of page g is slot
+ * n_pages * page <= 2^31 - 1; T * 2 * heads <= 2^31 - 1 and T * 2 * heads *
+ * head_dim <= 2^37 - 2^13 in a call. Token position `off` of page g is slot
  * g * page + off. `rotate` (0 or 1) must be the same in every call on a cache.
  *
  * qwha_cache_write: rows k[t][h][:] and v[t][h][:] (fp32 or bf16, [T][heads]
@@ -466,7 +467,9 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   is attended with, gives a row of out that holds no finite number (NaN, or for
  *   values an infinity). A score above fp32's range gives NaN, one below it
  *   weighs nothing, and a row all of whose scores lie below it is zeros.
- *   Requires heads to divide q_heads, 0 <= B <= 65535. Workspace:
+ *   Requires heads to divide q_heads, 0 <= B <= 65535, and a launch of less than
+ *   2^24 workgroups a sequence (QWHA_ERR_SHAPE beyond: where q_heads * width
+ *   passes about 2^34). Workspace:
  *   qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
  *   bytes (0 when out of range), 256-byte aligned; calls that may overlap
  *   need one each.

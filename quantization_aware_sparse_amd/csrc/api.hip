@@ -661,10 +661,14 @@ static qwha_status check_cache(int32_t heads, int32_t head_dim, int32_t bits, in
   return QWHA_OK;
 }
 
-// rows of a dense [T][2][heads] view, counted in int32 by the launches
-static qwha_status check_cache_tokens(int64_t T, int32_t heads) {
+// rows of a dense [T][2][heads] view, counted in int32 by the launches, whose
+// threads a grid has to hold
+static qwha_status check_cache_tokens(int64_t T, int32_t heads, int32_t head_dim) {
   if (T < 0 || T > INT32_MAX / (2 * static_cast<int64_t>(heads)))
     return fail(QWHA_ERR_SHAPE, "T=%lld: T * 2 * heads outside [0, 2^31 - 1]",
+                static_cast<long long>(T));
+  if (T * 2 * heads * (head_dim / kWritePer) > kMaxWriteThreads)
+    return fail(QWHA_ERR_SHAPE, "T=%lld: T * 2 * heads * head_dim outside [0, 2^37 - 2^13]",
                 static_cast<long long>(T));
   return QWHA_OK;
 }
@@ -677,7 +681,7 @@ qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64
   int lg_page;
   QWHA_TRY(check_cache(heads, head_dim, bits, rotate, n_pages, page, &lg_page));
   QWHA_TRY(check_dt(act, "act"));
-  QWHA_TRY(check_cache_tokens(T, heads));
+  QWHA_TRY(check_cache_tokens(T, heads, head_dim));
   QWHA_NEED(codes, 16);
   QWHA_NEED(scales, 4);
   QWHA_NEED(zeros, 4);
@@ -702,7 +706,7 @@ qwha_status qwha_cache_read(const uint32_t* codes, const float* scales, const fl
   int lg_page;
   QWHA_TRY(check_cache(heads, head_dim, bits, rotate, n_pages, page, &lg_page));
   QWHA_TRY(check_dt(out_dtype, "out_dtype"));
-  QWHA_TRY(check_cache_tokens(T, heads));
+  QWHA_TRY(check_cache_tokens(T, heads, head_dim));
   QWHA_NEED(codes, 16);
   QWHA_NEED(scales, 4);
   QWHA_NEED(zeros, 4);
@@ -725,7 +729,9 @@ size_t qwha_cache_attn_workspace_bytes(int32_t B, int32_t q_heads, int32_t heads
   if (B < 0 || B > 65535 || heads < 1 || heads > 4096 || q_heads < 1 || q_heads > 65535 ||
       q_heads % heads != 0 || width < 1 || page < 8 || page > 1024 ||
       static_cast<int64_t>(width) * page > INT32_MAX ||
-      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+      (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      cache_attn_blocks(B, q_heads, heads, head_dim, static_cast<int64_t>(width) * page, page) >
+          kMaxAttnBlocks)
     return 0;
   return align256(cache_attn_scratch_bytes(B, q_heads, heads, head_dim,
                                            static_cast<int64_t>(width) * page, page));
@@ -747,6 +753,10 @@ qwha_status qwha_cache_attn(const void* q, qwha_dtype act, int32_t B, int32_t q_
                 heads);
   if (width < 1 || static_cast<int64_t>(width) * page > INT32_MAX)
     return fail(QWHA_ERR_SHAPE, "width=%d: width * page outside [1, 2^31 - 1]", width);
+  if (cache_attn_blocks(B, q_heads, heads, head_dim, static_cast<int64_t>(width) * page, page) >
+      kMaxAttnBlocks)
+    return fail(QWHA_ERR_SHAPE, "width=%d of q_heads=%d needs 2^24 workgroups or more", width,
+                q_heads);
   if (!isfinite(scale)) return fail(QWHA_ERR_INVALID_ARG, "scale must be finite");
   QWHA_NEED(codes, 16);
   QWHA_NEED(scales, 4);

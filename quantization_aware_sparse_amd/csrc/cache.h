@@ -71,6 +71,11 @@ hipError_t by_shape(int dim, int bits, Fn&& fn) {
 // q_heads / heads query heads read each head; max_tokens = width * page
 size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t max_tokens,
                                 int page);
+// workgroups along the first dimension of a launch's grid, which holds 2^32 - 1 threads
+int64_t cache_attn_blocks(int B, int q_heads, int heads, int dim, int64_t max_tokens, int page);
+constexpr int64_t kMaxAttnBlocks = 0xFFFFFFFFll / 256;
+constexpr int kWritePer = 32;      // columns a lane of the writing kernel
+constexpr int64_t kMaxWriteThreads = 0xFFFFFFFFll - 255;
 hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,
                               const int32_t* slots, int rotate, const Cache& c, hipStream_t s);
 hipError_t launch_cache_read(const Cache& c, const int32_t* slots, int64_t T, int rotate, Dt dt,

@@ -71,8 +71,6 @@ __device__ __forceinline__ CallRow call_row(const Cache& c, uint32_t row) {
 // and sum), one within a lane a single one. 8192 tokens of 8 heads of 128 (33.5 MB
 // of bf16 in, 9.4 out): 15.9 us, of which the vector units' 35 instructions a
 // value take 15; at 4.9 TB/s the bytes take 8.8. 32 tokens: 3.8 us.
-constexpr int kWritePer = 32;
-
 template <int N, int BITS, typename TIn, bool ROT>
 __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict__ k,
                                                           const TIn* __restrict__ v, uint32_t rows,

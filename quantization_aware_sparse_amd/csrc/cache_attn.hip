@@ -589,6 +589,12 @@ size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t 
   return static_cast<size_t>(B) * q_heads * slices * (dim + 2) * sizeof(float);
 }
 
+int64_t cache_attn_blocks(int B, int q_heads, int heads, int dim, int64_t max_tokens, int page) {
+  const int per = q_heads / heads, ht = head_tiles(per, dim);
+  return static_cast<int64_t>(heads) * ((per + 4 * ht - 1) / (4 * ht)) *
+         attn_plan(B, q_heads, heads, dim, max_tokens, page).slices;
+}
+
 hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cache& c,
                              const int32_t* table, int width, const int32_t* lens, float scale,
                              int rotate, void* out, void* scratch, hipStream_t s) {
