@@ -467,15 +467,15 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   is attended with, gives a row of out that holds no finite number (NaN, or for
  *   values an infinity). A score above fp32's range gives NaN, one below it
  *   weighs nothing, and a row all of whose scores lie below it is zeros.
- *   Requires heads to divide q_heads, 0 <= B <= 65535, and a launch of less than
- *   2^24 workgroups a sequence (QWHA_ERR_SHAPE beyond: where q_heads * width
- *   passes about 2^34). Workspace:
+ *   Requires scale * log2(e) to be finite, heads to divide q_heads, 0 <= B <=
+ *   65535, and a launch of fewer than 2^24 workgroups a sequence (QWHA_ERR_SHAPE
+ *   beyond: where q_heads * width passes about 2^34). Workspace:
  *   qwha_cache_attn_workspace_bytes(B, q_heads, heads, head_dim, width, page)
  *   bytes (0 when out of range), 256-byte aligned; calls that may overlap
  *   need one each.
  * Values read (k, v, q, and the cache's rows in use) should be finite; others
- * spoil the rows said above and no more. Out-of-range slots and
- * pages are checked on the device and never read or written through.
+ * spoil the rows said above and no more. Out-of-range slots and pages are
+ * checked on the device and never read or written through.
  * --------------------------------------------------------------------------- */
 qwha_status qwha_cache_write(const void* k, const void* v, qwha_dtype act, int64_t T,
                              const int32_t* slots, int32_t heads, int32_t head_dim, int32_t bits,

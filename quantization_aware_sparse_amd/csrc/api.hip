@@ -757,7 +757,9 @@ qwha_status qwha_cache_attn(const void* q, qwha_dtype act, int32_t B, int32_t q_
       kMaxAttnBlocks)
     return fail(QWHA_ERR_SHAPE, "width=%d of q_heads=%d needs 2^24 workgroups or more", width,
                 q_heads);
-  if (!isfinite(scale)) return fail(QWHA_ERR_INVALID_ARG, "scale must be finite");
+  // the softmax runs on powers of two
+  if (!isfinite(scale * kLog2E))
+    return fail(QWHA_ERR_INVALID_ARG, "scale and scale * log2(e) must be finite");
   QWHA_NEED(codes, 16);
   QWHA_NEED(scales, 4);
   QWHA_NEED(zeros, 4);

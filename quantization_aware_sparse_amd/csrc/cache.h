@@ -74,6 +74,7 @@ size_t cache_attn_scratch_bytes(int B, int q_heads, int heads, int dim, int64_t 
 // workgroups along the first dimension of a launch's grid, which holds 2^32 - 1 threads
 int64_t cache_attn_blocks(int B, int q_heads, int heads, int dim, int64_t max_tokens, int page);
 constexpr int64_t kMaxAttnBlocks = 0xFFFFFFFFll / 256;
+constexpr float kLog2E = 1.44269504088896340736f;
 constexpr int kWritePer = 32;      // columns a lane of the writing kernel
 constexpr int64_t kMaxWriteThreads = 0xFFFFFFFFll - 255;
 hipError_t launch_cache_write(const void* k, const void* v, Dt dt, int64_t T,

@@ -606,7 +606,7 @@ hipError_t launch_cache_attn(const void* q, Dt dt, int B, int q_heads, const Cac
   a.table = table;
   a.width = width;
   a.lens = lens;
-  a.scale = scale * 1.44269504088896340736f;
+  a.scale = scale * kLog2E;
   a.rotate = rotate;
   const AttnPlan plan = attn_plan(B, q_heads, c.heads, c.dim,
                                   static_cast<int64_t>(width) << c.lg_page, 1 << c.lg_page);

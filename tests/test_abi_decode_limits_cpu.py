@@ -36,3 +36,8 @@ def test_rows_of_too_many_threads(q, heads, dim):
                               None) == SHAPE
     assert q.qwha_cache_read(FAKE, FAKE, FAKE, *args, 10, 16, FAKE, T, 1, FAKE, FAKE,
                              None) == SHAPE
+
+
+@pytest.mark.parametrize("scale", [3.0e38, -2.4e38, 3.4028234e38])
+def test_scales_whose_powers_of_two_pass_fp32(q, scale):
+    assert attn(q, scale=scale) == INVALID
