@@ -56,13 +56,4 @@ __device__ __forceinline__ bf16x8 operand8(uint32_t w0, uint32_t w1) {
   return as_operand(d);
 }
 
-// fp32 f as three bf16 numbers that sum to it exactly (8 bits of mantissa
-// each, what is left of f after the ones before, cut): word k, upper half
-__device__ __forceinline__ void split3(float f, uint32_t (&h)[3]) {
-  h[0] = __float_as_uint(f);
-  const float r = f - __uint_as_float(h[0] & 0xFFFF0000u);
-  h[1] = __float_as_uint(r);
-  h[2] = __float_as_uint(r - __uint_as_float(h[1] & 0xFFFF0000u));
-}
-
 }  // namespace qwha
