@@ -593,7 +593,11 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
 }
 
 size_t qwha_layer_decode_workspace_bytes(int64_t T, int32_t d_in, int32_t d_out, int64_t p) {
-  if (T < 0 || T > QWHA_DECODE_MAX_T || d_in < 1 || d_out < 1 || p < 0) return 0;
+  // every width of 64 columns and more is a multiple of 64 (check_width)
+  if (T < 0 || T > QWHA_DECODE_MAX_T || d_in < 64 || d_in > 16384 || d_in % 64 != 0 ||
+      d_out < 1 || d_out > (1 << 20) || p < 0 || p > INT32_MAX ||
+      p > static_cast<int64_t>(d_out) * d_in)
+    return 0;
   return align256(decode_scratch_bytes(static_cast<int>(T), d_in, d_out, p));
 }
 
@@ -727,7 +731,7 @@ qwha_status qwha_cache_read(const uint32_t* codes, const float* scales, const fl
 size_t qwha_cache_attn_workspace_bytes(int32_t B, int32_t q_heads, int32_t heads,
                                        int32_t head_dim, int32_t width, int32_t page) {
   if (B < 0 || B > 65535 || heads < 1 || heads > 4096 || q_heads < 1 || q_heads > 65535 ||
-      q_heads % heads != 0 || width < 1 || page < 8 || page > 1024 ||
+      q_heads % heads != 0 || width < 1 || page < 8 || page > 1024 || (page & (page - 1)) != 0 ||
       static_cast<int64_t>(width) * page > INT32_MAX ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
       cache_attn_blocks(B, q_heads, heads, head_dim, static_cast<int64_t>(width) * page, page) >

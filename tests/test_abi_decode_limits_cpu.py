@@ -41,3 +41,19 @@ def test_rows_of_too_many_threads(q, heads, dim):
 @pytest.mark.parametrize("scale", [3.0e38, -2.4e38, 3.4028234e38])
 def test_scales_whose_powers_of_two_pass_fp32(q, scale):
     assert attn(q, scale=scale) == INVALID
+
+
+def test_workspace_queries_out_of_range(q):
+    layer = q.qwha_layer_decode_workspace_bytes
+    assert layer(20, 256, 64, 500) > 0 and layer(64, 16384, 1 << 20, LAST) > 0
+    for d_in in (32, 100, 65, 16448, 1 << 30, LAST):
+        assert layer(20, d_in, 64, 500) == 0, d_in
+    for d_out in ((1 << 20) + 1, LAST):
+        assert layer(20, 256, d_out, 500) == 0, d_out
+    for p in (256 * 64 + 1, LAST + 1, 1 << 62):
+        assert layer(20, 256, 64, p) == 0, p
+    assert layer(20, 16384, 1 << 20, LAST + 1) == 0
+    rows = q.qwha_cache_attn_workspace_bytes
+    assert rows(1, 32, 8, 128, 1 << 16, 16) > 0
+    for page in (0, 4, 9, 24, 1000, 2048):
+        assert rows(1, 32, 8, 128, 1 << 16, page) == 0, page
