@@ -406,9 +406,11 @@ qwha_status qwha_layer_fwd(const void* x, qwha_dtype act, int64_t T, int32_t d_i
  * tokens (QWHA_ERR_SHAPE beyond: qwha_layer_fwd's tiles are the better fit
  * there). Weights, adapter and widths as qwha_layer_fwd (d_in >= 64, group >=
  * 32); x [T][d_in] and y [T][d_out] share `act`, QWHA_BF16 or QWHA_F32. The
- * codes come from memory once a call. Sums are fp32; fp32 x enters with its
- * 24 bits, a bf16 y is rounded once. p = 0 is the base layer alone (row_ptr, E
- * and c are then not read and may be NULL). Workspace:
+ * codes are read once per 16 bf16 or 4 fp32 tokens, or 64 and 16 where there are
+ * many of rows and tokens; what is read again comes from the caches where it
+ * fits. Sums are fp32; fp32 x enters with its 24 bits, those above 2^-126 (all of
+ * them from |x| = 2^-102 on), a bf16 y is rounded once. p = 0 is the base layer
+ * alone (row_ptr, E and c are then not read and may be NULL). Workspace:
  * qwha_layer_decode_workspace_bytes(T, d_in, d_out, p) bytes (0 when out of
  * range), 256-byte aligned; calls that may overlap need one each.
  * --------------------------------------------------------------------------- */
@@ -459,7 +461,8 @@ qwha_status qwha_layer_decode(const void* x, qwha_dtype act, int64_t T, int32_t 
  *   out [B][q_heads][head_dim] in `act`, table int32 [B][width], lens int32
  *   [B]. Sums and the softmax are fp32. q' = scale log2(e) q (times H with
  *   rotate), formed in fp32, enters with 32 bits counted from its head's largest
- *   component: each is off by 1.02 * 2^-31 of that one at most.
+ *   component: each is off by 1.02 * 2^-31 of that one at most. The weights times
+ *   the values' steps enter with 24 bits, those above 2^-126.
  *   lens[b] <= 0 gives a row of zeros, lens[b] above width * page counts as
  *   width * page, and the tokens of a table entry outside [0, n_pages) are
  *   left out. Nothing at or behind lens[b] is used, whatever it holds. A NaN or

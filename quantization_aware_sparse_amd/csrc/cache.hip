@@ -64,13 +64,14 @@ __device__ __forceinline__ CallRow call_row(const Cache& c, uint32_t row) {
 }
 
 // Bound by the vector units and then HBM: a row reads N elements and writes
-// N * b / 8 + 8 bytes. The transform runs in fp64: a row's sums are then exact
-// (16-bit inputs whose exponents span less than 2^37), so v, its range and
-// every code do not depend on the order of the additions. 32 columns a lane:
-// a stage across lanes costs 3 to 5 instructions a value (two moves, a product
-// and sum), one within a lane a single one. 8192 tokens of 8 heads of 128 (33.5 MB
-// of bf16 in, 9.4 out): 15.9 us, of which the vector units' 35 instructions a
-// value take 15; at 4.9 TB/s the bytes take 8.8. 32 tokens: 3.8 us.
+// N * b / 8 + 8 bytes. The transform runs in fp64: the sums of a row whose values
+// lie within 2^37 (bf16) or 2^21 (fp32) of each other are then exact, so that v,
+// its range and every code do not depend on the order of the additions. 32 columns
+// a lane: a stage across lanes costs 3 to 5 instructions a value (two moves, a
+// product and sum), one within a lane a single one. 8192 tokens of 8 heads of 128
+// (33.5 MB of bf16 in, 9.4 out): 16.9 us (median of twelve), of which the vector
+// units issue 31 instructions a value for 13.4 (at 2.4 GHz); at 4.9 TB/s the bytes
+// take 8.8. As fp32 19.3 us, the bytes 15.6. 32 tokens: 4.1 us.
 template <int N, int BITS, typename TIn, bool ROT>
 __global__ __launch_bounds__(256) void cache_write_kernel(const TIn* __restrict__ k,
                                                           const TIn* __restrict__ v, uint32_t rows,

@@ -27,11 +27,14 @@
 //             column whose code is its zero point leaves nothing, however large q';
 //   output  = sum p s_v (OFF + code) - sum p s_v (OFF + z_v).
 // A head's parts lie in one lane's results.
-// Bound by the vector units, which unpack: about 250 instructions of a wave for
-// 32 tokens of 128 columns, 9 KB of 4-bit keys and values. Measured (device time;
-// the cache's bytes at the 4.9 TB/s of a copy): 32 sequences of 1900 .. 4096 tokens,
-// 8 x 4 heads of 128, 4 bits 29.0 us of 22.7; 3 of up to 30001, 16 x 1 heads of 64,
-// 8 bits 23.1 + 4.1 us of 21; one of 777, 8 x 4 heads of 128 5.8 + 3.8 us of 0.2.
+// Bound by the bytes, and by the waves' waits for them between the vector
+// instructions that unpack: about 290 of a wave for 32 tokens of 128 columns, 9 KB
+// of 4-bit keys and values. Measured (median device time of twelve runs; the cache's
+// bytes at the 4.9 TB/s of a copy): 32 sequences of 1900 .. 4096 tokens, 8 x 4 heads
+// of 128, 4 bits 31.5 us of 22.7, of which vector instructions issue for 13.8 (at 2.4
+// GHz) and the matrix cores are busy for 1.9; waves wait half of their cycles. 3 of up
+// to 30001, 16 x 1 heads of 64, 8 bits 26.8 + 4.8 us of 21, 9.2 of them issue; one of
+// 777, 8 x 4 heads of 128 5.7 + 4.0 us of 0.2.
 //
 // cache_combine_kernel joins the slices: one maximum, one sum, one transform.
 //

@@ -7,14 +7,18 @@
 //                       K split over the waves of a workgroup; with few tokens
 //                       also the nonzeros of the same rows of F, the tokens
 //                       transformed by every workgroup for itself;
-//   decode_wide_kernel  more tokens, the codes read once for all of them: K split
+//   decode_wide_kernel  more tokens: 64 bf16 or 16 fp32 ones a workgroup, K split
 //                       over workgroups, partial sums;
 //   decode_finish_kernel  partial sums and the nonzeros of F added up.
-// Measured (device time; bytes that must move at the 4.9 TB/s of a copy):
-//   4096 x 4096,  4 bits, 1 token,   524288 nonzeros   8.6 us of 3.2, one launch;
-//   4096 x 14336, 4 bits, 3 tokens,  1179648          11.5 + 8.6 us of 9.7;
-//   14336 x 4096, 3 bits, 16 tokens, 1179648          18.4 + 12.4 us of 8.6;
-//   8192 x 8192,  2 bits, 64 tokens, 1048576          27.5 + 20.2 us of 7.8.
+// The codes are read and unpacked once per such tile of tokens (16 or 4, 64 or
+// 16): of the calls with several tiles the later ones find them in the caches,
+// where they fit.
+// Measured (median device time of twelve runs; bytes that must move at the 4.9
+// TB/s of a copy):
+//   4096 x 4096,  4 bits, 1 token,   524288 nonzeros   9.9 us of 3.2, one launch;
+//   4096 x 14336, 4 bits, 3 tokens,  1179648          13.2 + 8.9 us of 9.7;
+//   14336 x 4096, 3 bits, 16 tokens, 1179648          18.3 + 12.8 us of 8.6;
+//   8192 x 8192,  2 bits, 64 tokens, 1048576          27.6 + 20.8 us of 7.8.
 // Where z goes through memory, the first workgroups of the product's launch
 // write it, transposed (zt[column][token], so that one nonzero of F finds its
 // column's tokens side by side): the product does not need it, the finishing
@@ -28,7 +32,7 @@
 // bf16's 8 bits by themselves (OFF = 0). Products are exact in fp32; only the
 // fp32 additions round. fp32 tokens enter as three bf16 rows that sum to x
 // exactly (8 + 8 + 8 bits), which take otherwise idle rows of the matrix
-// instruction's 16.
+// instruction's 16; the instruction takes numbers below 2^-126 as zeros.
 #include <type_traits>
 
 #include "fwht_core.h"
@@ -714,10 +718,13 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const T* __restrict__ 
 // per workgroup, a wave 32 of them; the tokens' tiles are staged once for all
 // waves, and the spans are split over `slices` workgroups, whose partial sums
 // decode_finish_kernel adds up. Two spans are on their way while a third is
-// worked on: with one the kernel waits for memory at every span. Bound by the
-// vector units, which unpack for four tiles of tokens, and by the codes' latency
-// in about equal parts. Deeper queues do not fit the 256 registers: three spans
-// on their way 34.0 -> 38.6 us, four 44.6 (8192 x 8192, 4 bits, 64 tokens).
+// worked on: with one the kernel waits for memory at every span. Of 27.6 us (8192 x
+// 8192, 2 bits, 64 tokens; counters at 2.4 GHz) the vector instructions, most of
+// them unpacking and the groups' steps, issue for 9.1 and the matrix cores are busy
+// for 5.1; a SIMD's two waves wait for memory a third of their cycles, and the two
+// kinds of work of one wave do not overlap. Deeper queues do not fit the 256
+// registers: three spans on their way 34.0 -> 38.6 us, four 44.6 (8192 x 8192, 4
+// bits, 64 tokens).
 constexpr int kWideThreads = 256;
 constexpr int kWideRows = 128;
 constexpr int kWideTiles = 4;
@@ -1066,12 +1073,14 @@ int padded_tokens(int T) {
   return tp;
 }
 
-// Workgroups that share the spans of 128 rows: with those that write z (one or
-// more a token) two per compute unit, which is what fits at once, so that none
-// waits for a second turn; at least two spans each.
-int wide_slices(int z_blocks, int K, int N) {
+// Workgroups that share the spans of 128 rows: with one a token that writes z two
+// per compute unit, which is what fits at once; at least two spans each. Widths
+// that are not a power of two may have several workgroups a token for z: some of
+// the launch then wait for a second turn (4096 x 14336, 64 tokens: 448 of each
+// kind for 512 places, 52.2 us; 11008 columns 45.1).
+int wide_slices(int z_tokens, int K, int N) {
   const int tiles = (N + kWideRows - 1) / kWideRows, spans = (K + kSpan - 1) / kSpan;
-  const int want = (512 - z_blocks) / tiles, most = spans / 2;
+  const int want = (512 - z_tokens) / tiles, most = spans / 2;
   const int n = want < most ? want : most;
   return n < 1 ? 1 : n;
 }
